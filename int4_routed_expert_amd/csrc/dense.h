@@ -1,0 +1,61 @@
+// Kernel arguments and launchers of the dense operators (rows in int8, the int8
+// product, rotary positions).
+#pragma once
+
+#include "dot.h"
+
+namespace moe {
+
+// norm: x, residual, gamma, h; SwiGLU: x is the gate, residual the up rows.
+struct RowArgs {
+  int S, H;
+  float eps;
+  int g_bf16, y_bf16;
+  const void *x, *residual, *gamma;
+  void *h, *y;
+  int8_t *q;
+  float *d;
+  int64_t ldx, ldr, ldh, ldy, ldq;
+};
+
+struct QmmArgs {
+  int S, N, K, y_bf16;
+  const int8_t *q, *w;
+  const float *d, *dw;
+  void *y;
+  int64_t ldq, ldw, ldy;
+  int32_t *part;  // workspace
+};
+
+struct RopeArgs {
+  int S, D, half, offset, pos_i64;
+  float factor;
+  const void *pos;
+  const double *freqs;
+  moe_rope_tensor t[2];
+};
+
+// ---- elements of fp32 and bf16 rows ---------------------------------------------
+__device__ inline float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// fp32 to bf16, round to nearest even.
+__device__ inline uint16_t f_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+template <bool BF16>
+__device__ inline float load_el(const void *p, int64_t i) {
+  if constexpr (BF16) return bf16_f(ldg<uint16_t>((const uint16_t *)p + i));
+  else return ldg<float>((const float *)p + i);
+}
+template <bool BF16>
+__device__ inline void store_el(void *p, int64_t i, float v) {
+  if constexpr (BF16) stg<uint16_t>((uint16_t *)p + i, f_bf16(v));
+  else stg<float>((float *)p + i, v);
+}
+
+hipError_t launch_norm_quant(const RowArgs &a, int x_bf16, hipStream_t st);
+hipError_t launch_silu_quant(const RowArgs &a, int x_bf16, hipStream_t st);
+hipError_t launch_qmatmul(const QmmArgs &a, hipStream_t st);
+int64_t qmatmul_workspace(int S, int N, int K);
+hipError_t launch_rope(const RopeArgs &a, int x_bf16, int interleaved, hipStream_t st);
+
+}  // namespace moe

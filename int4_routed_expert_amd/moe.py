@@ -19,6 +19,8 @@ MOE_OK, MOE_EINVAL, MOE_ENULL, MOE_EDTYPE, MOE_EWORKSPACE, MOE_ENOSLOT, MOE_ESTA
     0, -1, -2, -3, -4, -5, -6, -7, -8
 MOE_F32, MOE_BF16 = 0, 1
 MOE_WF_Q4_G32, MOE_WF_Q4_ROW, MOE_WF_Q8_ROW = 0, 1, 2
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = 0, 1, 2, 3
 
 
 class MoeError(RuntimeError):
@@ -52,6 +54,12 @@ class moe_layer_call(ctypes.Structure):
                 ("ws_bytes", ctypes.c_size_t)]
 
 
+class moe_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built: run __graft_entry__.build() (hipcc for gfx950)")
@@ -62,7 +70,9 @@ def _load():
     import torch  # noqa: F401
     L = ctypes.CDLL(LIB_PATH)
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    f32, f64 = ctypes.c_float, ctypes.c_double
     cp = ctypes.POINTER(moe_cfg)
+    rp = ctypes.POINTER(moe_rope_tensor)
     sigs = {
         "moe_validate_cfg": (ctypes.c_int, [cp]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -90,6 +100,12 @@ def _load():
         "moe_pool_trace": (ctypes.c_int, [p, p, i32]),
         "moe_pool_stats": (ctypes.c_int, [p, ctypes.c_char_p, sz]),
         "moe_pool_check_view": (ctypes.c_int, [p, i32, ctypes.POINTER(moe_slot_view)]),
+        "moe_norm_quant": (ctypes.c_int, [p, i32, i64, p, i64, p, i32, f32, i32, i32, p, i64, p, i32, i64, p, i64, p, p]),
+        "moe_silu_quant": (ctypes.c_int, [p, p, i32, i64, i32, i32, p, i32, i64, p, i64, p, p]),
+        "moe_qmatmul_workspace_bytes": (i64, [i32, i32, i32]),
+        "moe_qmatmul": (ctypes.c_int, [p, i64, p, p, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
+        "moe_rope": (ctypes.c_int, [rp, rp, i32, i32, i32, i32, i32, i32, p, i32, p, f32, p]),
+        "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f32)]),
         "moe_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_profile_report": (ctypes.c_int, [ctypes.c_char_p, sz]),
     }
@@ -306,6 +322,261 @@ def moe_chain_launch(chain: int, stream=None) -> None:
 
 def moe_chain_destroy(chain: int | None) -> None:
     _lib.moe_chain_destroy(chain)
+
+
+# ---- dense operators ---------------------------------------------------------------------------------------------------
+
+def moe_norm_quant(x, x_dtype: int, ldx: int, residual, ldr: int, gamma, g_dtype: int, eps: float, S: int, H: int, h,
+                   ldh: int, y, y_dtype: int, ldy: int, q, ldq: int, d, stream=None) -> None:
+    _check(_lib.moe_norm_quant(ptr(x), x_dtype, ldx, ptr(residual), ldr, ptr(gamma), g_dtype, eps, S, H, ptr(h), ldh,
+                               ptr(y), y_dtype, ldy, ptr(q), ldq, ptr(d), stream_handle(stream)), "moe_norm_quant")
+
+
+def moe_silu_quant(g, u, x_dtype: int, ldx: int, S: int, I: int, y, y_dtype: int, ldy: int, q, ldq: int, d,
+                   stream=None) -> None:
+    _check(_lib.moe_silu_quant(ptr(g), ptr(u), x_dtype, ldx, S, I, ptr(y), y_dtype, ldy, ptr(q), ldq, ptr(d),
+                               stream_handle(stream)), "moe_silu_quant")
+
+
+def moe_qmatmul_workspace_bytes(S: int, N: int, K: int) -> int:
+    return _lib.moe_qmatmul_workspace_bytes(S, N, K)
+
+
+def moe_qmatmul(q, ldq: int, d, w, ldw: int, dw, S: int, N: int, K: int, y, y_dtype: int, ldy: int, ws, ws_bytes: int,
+                stream=None) -> None:
+    _check(_lib.moe_qmatmul(ptr(q), ldq, ptr(d), ptr(w), ldw, ptr(dw), S, N, K, ptr(y), y_dtype, ldy, ptr(ws), ws_bytes,
+                            stream_handle(stream)), "moe_qmatmul")
+
+
+def moe_rope(q: moe_rope_tensor, k: moe_rope_tensor | None, x_dtype: int, S: int, D: int, rot: int, offset: int,
+             layout: int, pos, pos_i64: int, freqs, factor: float, stream=None) -> None:
+    _check(_lib.moe_rope(ctypes.byref(q), None if k is None else ctypes.byref(k), x_dtype, S, D, rot, offset, layout,
+                         ptr(pos), pos_i64, ptr(freqs), factor, stream_handle(stream)), "moe_rope")
+
+
+def moe_rope_freqs(rot: int, theta: float, scaling: int, scale: float, trained_length: int, beta_fast: float,
+                   beta_slow: float):
+    """(float64 numpy array [rot / 2], factor)."""
+    import numpy as np
+    out = np.empty(max(rot, 0) // 2, np.float64)
+    factor = ctypes.c_float(0.0)
+    _check(_lib.moe_rope_freqs(rot, theta, scaling, scale, trained_length, beta_fast, beta_slow, ptr(out),
+                               ctypes.byref(factor)), "moe_rope_freqs")
+    return out, factor.value
+
+
+def _code(dtype, what: str) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+
+
+def _rows(t, shape, what: str) -> int:
+    """Row stride of the matrix t, whose rows must be contiguous (and, when shape is given, whose shape it must be)."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        want = "" if shape is None else f" of shape {list(shape)}"
+        raise ValueError(f"{what} must be a matrix{want} with contiguous rows, not {tuple(t.shape)} "
+                         f"with strides {tuple(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, n: int, dtype, what: str) -> None:
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}, not {tuple(t.shape)} {t.dtype}")
+
+
+def _one_device(first, *others):
+    """The GPU that every given tensor is on."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"the tensors must be on one GPU, not on {dev} and {t.device}")
+    return dev
+
+
+class _launch:
+    """Where a call that allocates its outputs launches: the tensors' GPU and the stream asked for (None: that GPU's
+    current one) become current, so that the outputs belong to the stream that writes them, and the inputs are kept
+    from reuse by their own streams until it is done with them."""
+
+    def __init__(self, dev, stream, *inputs):
+        import torch
+        self.contexts = []
+        if dev.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(stream, device=dev)
+            self.contexts.append(torch.cuda.stream(stream))
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+        self.dev = dev
+
+    def __enter__(self):
+        import torch
+        for c in self.contexts:
+            c.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *error):
+        for c in reversed(self.contexts):
+            c.__exit__(*error)
+
+
+def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant: bool = True, stream=None):
+    """(h, y, q, d) of the rows x [S, H]: moe_norm_quant with its outputs allocated on x's GPU.  h is the residual
+    sum (None without a residual; written over the tensor given as h, which may be residual or x), y the norm in
+    y_dtype (None: not wanted), q int8 and d fp32 the norm's quantised rows (None with quant=False)."""
+    import torch
+    xd, gd = _code(x.dtype, "x"), _code(gamma.dtype, "gamma")
+    ldx = _rows(x, None, "x")
+    S, H = x.shape
+    _vector(gamma, H, gamma.dtype, "gamma")
+    ldr = ldh = ldy = 0
+    if residual is not None:
+        ldr = _rows(residual, (S, H), "residual")
+        if residual.dtype != x.dtype:
+            raise ValueError(f"residual must have x's type {x.dtype}, not {residual.dtype}")
+    if h is not None:
+        if residual is None:
+            raise ValueError("h is the sum with a residual: none is given")
+        ldh = _rows(h, (S, H), "h")
+        if h.dtype != x.dtype:
+            raise ValueError(f"h must have x's type {x.dtype}, not {h.dtype}")
+    yd = MOE_F32 if y_dtype is None else _code(y_dtype, "y_dtype")
+    if residual is None and y_dtype is None and not quant:
+        raise ValueError("no output is asked for")
+    dev = _one_device(x, gamma, residual, h)
+    with _launch(dev, stream, x, gamma, residual, h) as st:
+        if residual is not None and h is None:
+            h, ldh = torch.empty((S, H), dtype=x.dtype, device=dev), H
+        y = torch.empty((S, H), dtype=y_dtype, device=dev) if y_dtype is not None else None
+        q = torch.empty((S, H), dtype=torch.int8, device=dev) if quant else None
+        d = torch.empty(S, dtype=torch.float32, device=dev) if quant else None
+        moe_norm_quant(x, xd, ldx, residual, ldr, gamma, gd, eps, S, H, h, ldh, y, yd, H, q, H, d, st)
+    return h, y, q, d
+
+
+def silu_quant(g, u=None, y_dtype=None, quant: bool = True, stream=None):
+    """(y, q, d) of silu(g) * u, both [S, I], or of the halves of g [S, 2 I] where u is None: moe_silu_quant with its
+    outputs allocated on g's GPU.  y in y_dtype (None: not wanted), q int8 and d fp32 (None with quant=False)."""
+    import torch
+    xd, ldx = _code(g.dtype, "g"), _rows(g, None, "g")
+    S, I = g.shape
+    if u is None:
+        if I % 2:
+            raise ValueError(f"g holds gate and up side by side: its width {I} must be even")
+        I //= 2
+        up = ptr(g) + I * g.element_size() if S else None
+    else:
+        if u.dtype != g.dtype:
+            raise ValueError(f"u must have g's type {g.dtype}, not {u.dtype}")
+        if _rows(u, (S, I), "u") != ldx:
+            raise ValueError(f"u must have g's row stride {ldx}, not {u.stride(0)}")
+        up = ptr(u)
+    yd = MOE_F32 if y_dtype is None else _code(y_dtype, "y_dtype")
+    if y_dtype is None and not quant:
+        raise ValueError("no output is asked for")
+    dev = _one_device(g, u)
+    with _launch(dev, stream, g, u) as st:
+        y = torch.empty((S, I), dtype=y_dtype, device=dev) if y_dtype is not None else None
+        q = torch.empty((S, I), dtype=torch.int8, device=dev) if quant else None
+        d = torch.empty(S, dtype=torch.float32, device=dev) if quant else None
+        moe_silu_quant(g, up, xd, ldx, S, I, y, yd, I, q, I, d, st)
+    return y, q, d
+
+
+def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
+    """y [S, N] in out_dtype (bfloat16 unless given): moe_qmatmul of the int8 rows q [S, K] with scales d [S] and the
+    int8 weights w [N, K] with scales dw [N], with its output (and, when ws is None, a workspace) allocated on q's
+    GPU."""
+    import torch
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    yd = _code(out_dtype, "out_dtype")
+    ldq = _rows(q, None, "q")
+    S, K = q.shape
+    if w.dim() != 2:
+        raise ValueError(f"w must be a matrix, not {tuple(w.shape)}")
+    N = w.shape[0]
+    ldw = _rows(w, (N, K), "w")
+    if q.dtype != torch.int8 or w.dtype != torch.int8:
+        raise ValueError(f"q and w must be int8, not {q.dtype} and {w.dtype}")
+    _vector(d, S, torch.float32, "d")
+    _vector(dw, N, torch.float32, "dw")
+    dev = _one_device(q, d, w, dw, ws)
+    need = moe_qmatmul_workspace_bytes(S, N, K)
+    if need < 0:
+        raise MoeError(need, "moe_qmatmul")
+    with _launch(dev, stream, q, d, w, dw, ws) as st:
+        if need and ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        y = torch.empty((S, N), dtype=out_dtype, device=dev)
+        moe_qmatmul(q, ldq, d, w, ldw, dw, S, N, K, y, yd, N, ws, ws.numel() * ws.element_size() if need else 0, st)
+    return y
+
+
+_ROPE_SCALING = {"none": MOE_ROPE_PLAIN, "linear": MOE_ROPE_LINEAR, "ntk": MOE_ROPE_NTK, "yarn": MOE_ROPE_YARN}
+
+
+def rope_freqs(rot: int, theta: float = 10000.0, scaling: str = "none", scale: float = 1.0, trained_length: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(freqs, factor) for rope: moe_rope_freqs with the frequencies as a float64 tensor on `device`."""
+    import torch
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}, not {scaling!r}")
+    f, factor = moe_rope_freqs(rot, theta, _ROPE_SCALING[scaling], scale, trained_length, beta_fast, beta_slow)
+    return torch.from_numpy(f).to(device), factor
+
+
+def _heads(t, S: int, D: int, what: str) -> None:
+    if t.dim() != 3 or t.shape[0] != S or t.shape[2] != D or (D > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [{S}, heads, {D}] with contiguous heads, not {tuple(t.shape)} "
+                         f"with strides {tuple(t.stride())}")
+
+
+def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: float = 1.0, inplace: bool = False,
+         stream=None):
+    """(q, k) turned to their positions: moe_rope of q [S, heads, D] and k [S, kheads, D] (or None), with pos [S] int32
+    or int64 and freqs [rot / 2] float64, into tensors allocated on q's GPU, or over q and k with inplace=True."""
+    import torch
+    xd = _code(q.dtype, "q")
+    S, D = q.shape[0], q.shape[-1]
+    _heads(q, S, D, "q")
+    if k is not None:
+        _heads(k, S, D, "k")
+        if k.dtype != q.dtype:
+            raise ValueError(f"k must have q's type {q.dtype}, not {k.dtype}")
+    if pos.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"pos must be int32 or int64, not {pos.dtype}")
+    _vector(pos, S, pos.dtype, "pos")
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs must be a vector, not {tuple(freqs.shape)}")
+    _vector(freqs, freqs.shape[0], torch.float64, "freqs")
+    dev = _one_device(q, k, pos, freqs)
+    with _launch(dev, stream, q, k, pos, freqs) as st:
+        outs, args = [], []
+        for t in (q, k):
+            if t is None or t.shape[1] == 0:
+                outs.append(t)
+                args.append(None)
+                continue
+            o = t if inplace else torch.empty(t.shape, dtype=t.dtype, device=dev)
+            outs.append(o)
+            s0, s1, _ = t.stride()
+            o0, o1 = (s0, s1) if inplace else (t.shape[1] * D, D)
+            args.append(moe_rope_tensor(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, t.shape[1]))
+        if args[0] is None:
+            raise ValueError("q has no heads")
+        moe_rope(args[0], args[1], xd, S, D, 2 * freqs.shape[0], offset,
+                 MOE_ROPE_INTERLEAVED if interleaved else MOE_ROPE_HALF, pos, int(pos.dtype == torch.int64), freqs,
+                 factor, st)
+    return outs[0], outs[1]
 
 
 def moe_profile_enable(on: bool) -> None:
