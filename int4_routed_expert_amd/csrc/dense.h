@@ -20,6 +20,7 @@ struct RowArgs {
 
 struct QmmArgs {
   int S, N, K, y_bf16;
+  int y_vec;  // four neighbouring outputs may be stored at once
   const int8_t *q, *w;
   const float *d, *dw;
   void *y;

@@ -5,33 +5,310 @@
 namespace moe {
 namespace {
 
-// One wave per output.
-__global__ __launch_bounds__(256) void k_qmm_plain(QmmArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t n_out = (int64_t)a.S * a.N;
-  for (int64_t o = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); o < n_out; o += (int64_t)gridDim.x * 4) {
-    const int64_t s = o / a.N, n = o - s * a.N;
-    const int8_t *q = a.q + s * a.ldq, *w = a.w + n * a.ldw;
-    int sum = 0;
-    for (int k = lane; k < a.K; k += 64) sum += (int)ldg<int8_t>(q + k) * (int)ldg<int8_t>(w + k);
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef u32x4_t u32x4_any __attribute__((aligned(1)));
+
+__device__ const uint8_t g_zeros[16] __attribute__((aligned(16))) = {};
+
+// 16 bytes at any address.
+__device__ inline i32x4 load16(const int8_t *p) {
+  return __builtin_bit_cast(i32x4, *(const __attribute__((address_space(1))) u32x4_any *)p);
+}
+
+// Bytes [k, k + 16) of a row of K bytes, zeros beyond its end.  The row's last, partial
+// chunk is read as the 16 bytes that end with it and shifted down, so nothing beyond the
+// row is touched.
+__device__ inline i32x4 load16_tail(const int8_t *row, int k, int K) {
+  i32x4 v = {0, 0, 0, 0};
+  if (k + 16 <= K) return load16(row + k);
+  if (k >= K) return v;
+  if (K >= 16) {
+    const u32x4_t r = __builtin_bit_cast(u32x4_t, load16(row + K - 16));
+    const int drop = k + 16 - K;  // 1..15 bytes of the previous chunk in front
+    unsigned __int128 x = ((unsigned __int128)(((uint64_t)r.w << 32) | r.z) << 64) | (((uint64_t)r.y << 32) | r.x);
+    x >>= 8 * drop;
+    return i32x4{(int)(uint32_t)x, (int)(uint32_t)(x >> 32), (int)(uint32_t)(x >> 64), (int)(uint32_t)(x >> 96)};
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int j = k; j < K; ++j) w[(j - k) >> 2] |= (uint32_t)(uint8_t)ldg<int8_t>(row + j) << (8 * ((j - k) & 3));
+  return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+}
+
+// Four neighbouring outputs y[s, n .. n + 3], those below N.
+__device__ inline void store4(const QmmArgs &a, int64_t s, int n, float v0, float v1, float v2, float v3) {
+  const float v[4] = {v0, v1, v2, v3};
+  if (a.y_vec && n + 4 <= a.N) {
+    if (a.y_bf16) {
+      const uint2 p = make_uint2((uint32_t)f_bf16(v0) | ((uint32_t)f_bf16(v1) << 16),
+                                 (uint32_t)f_bf16(v2) | ((uint32_t)f_bf16(v3) << 16));
+      *(__attribute__((address_space(1))) uint64_t *)((uint16_t *)a.y + s * a.ldy + n) = ((uint64_t)p.y << 32) | p.x;
+    } else {
+      stg<float4>((float *)a.y + s * a.ldy + n, make_float4(v0, v1, v2, v3));
+    }
+  } else {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    if (lane == 0) {
-      const float v = (float)sum * (a.d[s] * a.dw[n]);
-      if (a.y_bf16) stg<uint16_t>((uint16_t *)a.y + s * a.ldy + n, f_bf16(v));
-      else stg<float>((float *)a.y + s * a.ldy + n, v);
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) {
+        if (a.y_bf16) store_el<true>(a.y, s * a.ldy + n + j, v[j]);
+        else store_el<false>(a.y, s * a.ldy + n + j, v[j]);
+      }
+  }
+}
+
+// ---- few tokens ------------------------------------------------------------------
+// A workgroup takes 16 MT weight rows and all the tokens (NT blocks of 16); its waves
+// split K and add their int32 sums in LDS.  v_mfma_i32_16x16x64_i8 with the weights as
+// rows and the tokens as columns, both operands straight from memory: lane l holds 16
+// bytes of row (or token) l % 16 at k + 16 (l / 16).
+template <int MT, int NT, int W>
+__global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
+  constexpr int kU = MT * NT >= 4 ? 2 : 4;  // k steps in flight
+  __shared__ i32x4 s_acc[W][MT * NT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16 * MT, s0 = blockIdx.y * 16 * NT;
+  const int col = lane & 15, kq = (lane >> 4) * 16;
+  const int8_t *wr[MT], *qr[NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) wr[m] = a.w + (int64_t)min(n0 + 16 * m + col, a.N - 1) * a.ldw + kq;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) qr[t] = a.q + (int64_t)min(s0 + 16 * t + col, a.S - 1) * a.ldq + kq;
+  i32x4 acc[MT][NT] = {};
+  // whole steps of 64 bytes shared out evenly; the last wave takes the partial one
+  const int steps = a.K / 64;
+  const int lo = (int)((int64_t)steps * wave / W), hi = (int)((int64_t)steps * (wave + 1) / W);
+  int st = lo;
+  for (; st + kU <= hi; st += kU) {
+    i32x4 A[kU][MT], B[kU][NT];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) A[u][m] = load16(wr[m] + (st + u) * 64);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) B[u][t] = load16(qr[t] + (st + u) * 64);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[u][m], B[u][t], acc[m][t], 0, 0, 0);
+  }
+  for (; st < hi; ++st) {
+    i32x4 A[MT], B[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) A[m] = load16(wr[m] + st * 64);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) B[t] = load16(qr[t] + st * 64);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[m], B[t], acc[m][t], 0, 0, 0);
+  }
+  if (wave == W - 1 && steps * 64 < a.K) {
+    i32x4 A[MT], B[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) A[m] = load16_tail(wr[m] - kq, steps * 64 + kq, a.K);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) B[t] = load16_tail(qr[t] - kq, steps * 64 + kq, a.K);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[m], B[t], acc[m][t], 0, 0, 0);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s_acc[wave][m * NT + t][lane] = acc[m][t];
+  __syncthreads();
+  for (int b = wave; b < MT * NT; b += W) {
+    i32x4 sum = s_acc[0][b][lane];
+#pragma unroll
+    for (int v = 1; v < W; ++v) sum += s_acc[v][b][lane];
+    const int s = s0 + 16 * (b % NT) + col, n = n0 + 16 * (b / NT) + (lane >> 4) * 4;
+    if (s < a.S && n < a.N) {
+      const float ds = ldg<float>(a.d + s);
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = (float)sum[j] * (ds * ldg<float>(a.dw + min(n + j, a.N - 1)));
+      store4(a, s, n, v[0], v[1], v[2], v[3]);
     }
   }
+}
+
+// ---- many tokens -----------------------------------------------------------------
+// A workgroup of WN x WS waves takes BN weight rows x BS tokens, each wave its
+// (BN / WN) x (BS / WS) part in blocks of v_mfma_i32_32x32x32_i8 (weights as rows, tokens
+// as columns).  Both operands go through LDS in stages of 64 bytes of K, NBUF of them:
+// stage s + NBUF is requested as soon as stage s has been read.
+constexpr int kBK = 64;
+constexpr int kXcds = 8;
+
+// Where the 16-byte chunk c of a stage's row r lies: the rows' chunks are permuted so that
+// lanes reading one chunk of neighbouring rows spread over the banks.
+__device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ ((r >> 1) & 3)) << 4); }
+
+template <int BN, int BS, int WN, int WS, int NBUF, bool DIRECT>
+__global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
+  constexpr int kThr = 64 * WN * WS;
+  constexpr int TN = BN / WN / 32, TS = BS / WS / 32;  // 32x32 blocks of a wave
+  constexpr int kRows = BN + BS, kStage = kRows * kBK;
+  constexpr int kPer = kStage / 16 / kThr;  // chunks a thread moves per stage
+  static_assert(kStage % (16 * kThr) == 0, "stage split");
+  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage];
+  __shared__ float s_sc[kRows];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wn = wave / WS, wsv = wave % WS;
+
+  // Blocks go to the XCDs round-robin; each XCD gets a contiguous run of tiles, ordered in
+  // strips of `group` token tiles so that the tiles in flight on it share operands in its L2.
+  const int total = tiles_n * tiles_s;
+  const int per = (total + kXcds - 1) / kXcds;
+  const int t = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+  if ((int)(blockIdx.x / kXcds) >= per || t >= total) return;
+  const int strip = t / (group * tiles_n), in = t - strip * group * tiles_n;
+  const int g = min(group, tiles_s - strip * group);
+  const int ts = strip * group + in % g, tn = in / g;
+  const int n0 = tn * BN, s0 = ts * BS;
+
+  // this thread's chunks of a stage: LDS position threadIdx.x + i kThr, which holds chunk
+  // c of row r
+  const int8_t *src[kPer];
+  int kc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = threadIdx.x + i * kThr, r = p >> 2;
+    kc[i] = ((p & 3) ^ ((r >> 1) & 3)) << 4;
+    src[i] = r < BN ? a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw : a.q + (int64_t)min(s0 + r - BN, a.S - 1) * a.ldq;
+  }
+  const int stages = (a.K + kBK - 1) / kBK;
+  const int whole = a.K / kBK;
+
+  auto request = [&](int s) {  // DIRECT: stage s into its buffer
+    uint8_t *base = s_buf + (s % NBUF) * kStage + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int8_t *p = src[i] + (int64_t)s * kBK + kc[i];
+      if (s >= whole && s * kBK + kc[i] >= a.K) p = (const int8_t *)g_zeros;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
+                                       (__attribute__((address_space(3))) void *)(base + i * kThr * 16), 16, 0, 0);
+    }
+  };
+
+  i32x16 acc[TN][TS];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TS; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+
+  const int row = lane & 31, ck = lane >> 5;
+  auto frag = [&](const uint8_t *buf, int r, int kk) {
+    return *(const i32x4 *)(buf + chunk_of(r, kk * 2 + ck));
+  };
+  auto step = [&](const uint8_t *buf) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      i32x4 A[TN], B[TS];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) A[i] = frag(buf, wn * (BN / WN) + i * 32 + row, kk);
+#pragma unroll
+      for (int j = 0; j < TS; ++j) B[j] = frag(buf, BN + wsv * (BS / WS) + j * 32 + row, kk);
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TS; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  if constexpr (DIRECT) {
+    for (int s = 0; s < NBUF - 1; ++s)
+      if (s < stages) request(s);
+    for (int s = 0; s < stages; ++s) {
+      __syncthreads();
+      if (s + NBUF - 1 < stages) request(s + NBUF - 1);
+      step(s_buf + (s % NBUF) * kStage);
+    }
+  } else {
+    i32x4 v[kPer];
+    auto fetch = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        v[i] = s < whole ? load16(src[i] + (int64_t)s * kBK + kc[i]) : load16_tail(src[i], s * kBK + kc[i], a.K);
+    };
+    auto put = [&](int s) {
+      uint8_t *base = s_buf + (s % NBUF) * kStage;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) *(i32x4 *)(base + (threadIdx.x + i * kThr) * 16) = v[i];
+    };
+    fetch(0);
+    put(0);
+    for (int s = 0; s < stages; ++s) {
+      if (s + 1 < stages) fetch(s + 1);
+      __syncthreads();
+      step(s_buf + (s % NBUF) * kStage);
+      if (s + 1 < stages) put(s + 1);
+    }
+  }
+
+  for (int i = threadIdx.x; i < kRows; i += kThr)
+    s_sc[i] = i < BN ? ldg<float>(a.dw + min(n0 + i, a.N - 1)) : ldg<float>(a.d + min(s0 + i - BN, a.S - 1));
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < TS; ++j) {
+    const int sl = wsv * (BS / WS) + j * 32 + row;
+    const float ds = s_sc[BN + sl];
+    if (s0 + sl < a.S) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nl = wn * (BN / WN) + i * 32 + 8 * e + 4 * ck;
+          if (n0 + nl < a.N)
+            store4(a, s0 + sl, n0 + nl, (float)acc[i][j][4 * e] * (ds * s_sc[nl]),
+                   (float)acc[i][j][4 * e + 1] * (ds * s_sc[nl + 1]), (float)acc[i][j][4 * e + 2] * (ds * s_sc[nl + 2]),
+                   (float)acc[i][j][4 * e + 3] * (ds * s_sc[nl + 3]));
+        }
+    }
+  }
+}
+
+template <int MT, int NT, int W>
+void launch_few(const QmmArgs &a, hipStream_t st) {
+  const dim3 g((unsigned)((a.N + 16 * MT - 1) / (16 * MT)), (unsigned)((a.S + 16 * NT - 1) / (16 * NT)));
+  MOE_LAUNCH((k_qmm_few<MT, NT, W>), g, dim3(64 * W), 0, st, a);
+}
+
+template <int BN, int BS, int WN, int WS, int NBUF>
+void launch_tile(const QmmArgs &a, bool direct, hipStream_t st) {
+  const int tn = (a.N + BN - 1) / BN, ts = (a.S + BS - 1) / BS;
+  const int64_t total = (int64_t)tn * ts;
+  const dim3 g((unsigned)((total + kXcds - 1) / kXcds * kXcds));
+  const int group = 4;
+  if (direct) MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, NBUF, true>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
+  else MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, 2, false>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
 }
 
 }  // namespace
 
 int64_t qmatmul_workspace(int, int, int) { return 0; }
 
-hipError_t launch_qmatmul(const QmmArgs &a, hipStream_t st) {
+hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
   ProfScope ps("qmatmul", st);
-  const int64_t blocks = ((int64_t)a.S * a.N + 3) / 4;
-  MOE_LAUNCH(k_qmm_plain, dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)), dim3(256), 0, st, a);
+  QmmArgs a = a0;
+  a.y_vec = (uintptr_t)a.y % (a.y_bf16 ? 8 : 16) == 0 && a.ldy % 4 == 0;
+  const bool direct = (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.K % 16 == 0;
+  if (a.S <= 16) launch_few<1, 1, 8>(a, st);
+  else if (a.S <= 32) launch_few<1, 2, 8>(a, st);
+  else if (a.S <= 64) launch_few<1, 4, 8>(a, st);
+  else if ((int64_t)((a.N + 255) / 256) * ((a.S + 255) / 256) >= 192) launch_tile<256, 256, 2, 2, 4>(a, direct, st);
+  else if ((int64_t)((a.N + 127) / 128) * ((a.S + 127) / 128) >= 192) launch_tile<128, 128, 2, 2, 4>(a, direct, st);
+  else launch_tile<64, 64, 2, 2, 4>(a, direct, st);
   return hipGetLastError();
 }
 
