@@ -151,6 +151,17 @@ constexpr int kXcds = 8;
 // lanes reading one chunk of neighbouring rows spread over the banks.
 __device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ ((r >> 1) & 3)) << 4); }
 
+// One 16-byte load per lane from p straight into LDS, to lds + 16 lane (lds wave-uniform).
+__device__ inline void load_to_lds(const int8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(p) : "memory");
+}
+
+// Waits until at most N of this wave's loads are in flight and its reads of LDS are done.
+template <int N>
+__device__ inline void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 template <int BN, int BS, int WN, int WS, int NBUF, bool DIRECT>
 __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
   constexpr int kThr = 64 * WN * WS;
@@ -158,8 +169,10 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   constexpr int kRows = BN + BS, kStage = kRows * kBK;
   constexpr int kPer = kStage / 16 / kThr;  // chunks a thread moves per stage
   static_assert(kStage % (16 * kThr) == 0, "stage split");
-  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage];
-  __shared__ float s_sc[kRows];
+  constexpr int kWide = BN / WN, kLd = kWide + 4;  // a wave's weights, and what a token's sums of them take in LDS
+  constexpr int kTurn = WN * WS * 32 * kLd * 4;
+  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage > kTurn ? NBUF * kStage : kTurn];
+  __shared__ __align__(16) float s_sc[kRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wn = wave / WS, wsv = wave % WS;
 
@@ -187,17 +200,6 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   const int stages = (a.K + kBK - 1) / kBK;
   const int whole = a.K / kBK;
 
-  auto request = [&](int s) {  // DIRECT: stage s into its buffer
-    uint8_t *base = s_buf + (s % NBUF) * kStage + wave * 1024;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int8_t *p = src[i] + (int64_t)s * kBK + kc[i];
-      if (s >= whole && s * kBK + kc[i] >= a.K) p = (const int8_t *)g_zeros;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
-                                       (__attribute__((address_space(3))) void *)(base + i * kThr * 16), 16, 0, 0);
-    }
-  };
-
   i32x16 acc[TN][TS];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
@@ -207,33 +209,56 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
   const int row = lane & 31, ck = lane >> 5;
-  auto frag = [&](const uint8_t *buf, int r, int kk) {
+  // fragment f of a stage's k step: the wave's TN weight blocks, then its TS token blocks
+  auto frag = [&](const uint8_t *buf, int f, int kk) {
+    const int r = (f < TN ? wn * (BN / WN) + f * 32 : BN + wsv * (BS / WS) + (f - TN) * 32) + row;
     return *(const i32x4 *)(buf + chunk_of(r, kk * 2 + ck));
-  };
-  auto step = [&](const uint8_t *buf) {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      i32x4 A[TN], B[TS];
-#pragma unroll
-      for (int i = 0; i < TN; ++i) A[i] = frag(buf, wn * (BN / WN) + i * 32 + row, kk);
-#pragma unroll
-      for (int j = 0; j < TS; ++j) B[j] = frag(buf, BN + wsv * (BS / WS) + j * 32 + row, kk);
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TS; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
-    }
   };
 
   if constexpr (DIRECT) {
-    for (int s = 0; s < NBUF - 1; ++s)
-      if (s < stages) request(s);
+    // The wait for a stage leaves the requests of the stages after it in flight, so the
+    // requests are written in assembly: a load into LDS known to the compiler makes it
+    // wait for all of them before the next read of LDS.  Beyond K a request reads zeros.
+    constexpr int kF = TN + TS, kM = TN * TS;
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024;
+    auto request = [&](int i, int s) {
+      const int8_t *p = src[i] + (int64_t)s * kBK + kc[i];
+      if (s >= whole && (int64_t)s * kBK + kc[i] >= a.K) p = (const int8_t *)g_zeros;
+      load_to_lds(p, lds + (s % NBUF) * kStage + i * kThr * 16);
+    };
+    for (int s = 0; s < NBUF; ++s)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) request(i, s);
+    wait_loads<(NBUF - 1) * kPer>();
+    __builtin_amdgcn_s_barrier();
+    i32x4 F[2][kF];
+#pragma unroll
+    for (int f = 0; f < kF; ++f) F[0][f] = frag(s_buf, f, 0);
+    // Half a stage: multiply one k step's fragments while the next step's are read and,
+    // in the second half, the stage just read is requested anew, spread between the MFMAs.
+    auto half = [&](int cur, const uint8_t *buf, int kk, int again) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+#pragma unroll
+        for (int f = 0; f < kF; ++f)
+          if (f * kM / kF == m) F[cur ^ 1][f] = frag(buf, f, kk);
+        if (again >= 0) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (i * kM / kPer == m) request(i, again);
+        }
+        acc[m / TS][m % TS] =
+            __builtin_amdgcn_mfma_i32_32x32x32_i8(F[cur][m / TS], F[cur][TN + m % TS], acc[m / TS][m % TS], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
     for (int s = 0; s < stages; ++s) {
-      __syncthreads();
-      if (s + NBUF - 1 < stages) request(s + NBUF - 1);
-      step(s_buf + (s % NBUF) * kStage);
+      half(0, s_buf + (s % NBUF) * kStage, 1, -1);
+      wait_loads<(NBUF - 2) * kPer>();
+      __builtin_amdgcn_s_barrier();
+      half(1, s_buf + ((s + 1) % NBUF) * kStage, 0, s + NBUF);
     }
+    wait_loads<0>();
   } else {
     i32x4 v[kPer];
     auto fetch = [&](int s) {
@@ -251,30 +276,52 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
     for (int s = 0; s < stages; ++s) {
       if (s + 1 < stages) fetch(s + 1);
       __syncthreads();
-      step(s_buf + (s % NBUF) * kStage);
+      const uint8_t *buf = s_buf + (s % NBUF) * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        i32x4 A[TN], B[TS];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) A[i] = frag(buf, i, kk);
+#pragma unroll
+        for (int j = 0; j < TS; ++j) B[j] = frag(buf, TN + j, kk);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TS; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
+      }
       if (s + 1 < stages) put(s + 1);
     }
   }
 
+  // Each wave turns its sums round in its own part of the buffers, 32 tokens at a time, so
+  // that they leave as runs of a token's neighbouring outputs.
   for (int i = threadIdx.x; i < kRows; i += kThr)
     s_sc[i] = i < BN ? ldg<float>(a.dw + min(n0 + i, a.N - 1)) : ldg<float>(a.d + min(s0 + i - BN, a.S - 1));
   __syncthreads();
+  int *out = (int *)s_buf + wave * 32 * kLd;
+  constexpr int kRun = kWide / 4, kTok = 64 / kRun;  // lanes of a token's run, tokens at a time
 #pragma unroll
   for (int j = 0; j < TS; ++j) {
-    const int sl = wsv * (BS / WS) + j * 32 + row;
-    const float ds = s_sc[BN + sl];
-    if (s0 + sl < a.S) {
 #pragma unroll
-      for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nl = wn * (BN / WN) + i * 32 + 8 * e + 4 * ck;
-          if (n0 + nl < a.N)
-            store4(a, s0 + sl, n0 + nl, (float)acc[i][j][4 * e] * (ds * s_sc[nl]),
-                   (float)acc[i][j][4 * e + 1] * (ds * s_sc[nl + 1]), (float)acc[i][j][4 * e + 2] * (ds * s_sc[nl + 2]),
-                   (float)acc[i][j][4 * e + 3] * (ds * s_sc[nl + 3]));
-        }
+      for (int e = 0; e < 4; ++e)
+        *(i32x4 *)(out + row * kLd + i * 32 + 8 * e + 4 * ck) =
+            i32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+    __builtin_amdgcn_wave_barrier();
+    const int nl = wn * kWide + (lane % kRun) * 4;
+    const float4 dw = *(const float4 *)(s_sc + nl);
+#pragma unroll 4
+    for (int r = lane / kRun; r < 32; r += kTok) {
+      const int sl = wsv * (BS / WS) + j * 32 + r;
+      const i32x4 v = *(const i32x4 *)(out + r * kLd + (lane % kRun) * 4);
+      const float ds = s_sc[BN + sl];
+      if (s0 + sl < a.S && n0 + nl < a.N)
+        store4(a, s0 + sl, n0 + nl, (float)v[0] * (ds * dw.x), (float)v[1] * (ds * dw.y), (float)v[2] * (ds * dw.z),
+               (float)v[3] * (ds * dw.w));
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
