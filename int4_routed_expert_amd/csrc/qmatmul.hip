@@ -144,12 +144,18 @@ __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
 // (BN / WN) x (BS / WS) part in blocks of v_mfma_i32_32x32x32_i8 (weights as rows, tokens
 // as columns).  Both operands go through LDS in stages of 64 bytes of K, NBUF of them:
 // stage s + NBUF is requested as soon as stage s has been read.
-constexpr int kBK = 64;
 constexpr int kXcds = 8;
 
 // Where the 16-byte chunk c of a stage's row r lies: the rows' chunks are permuted so that
 // lanes reading one chunk of neighbouring rows spread over the banks.
-__device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ ((r >> 1) & 3)) << 4); }
+template <int BK>
+__device__ inline int mix_of(int r) {
+  return BK == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
+}
+template <int BK>
+__device__ inline int chunk_of(int r, int c) {
+  return r * BK + ((c ^ mix_of<BK>(r)) << 4);
+}
 
 // One 16-byte load per lane from p straight into LDS, to lds + 16 lane (lds wave-uniform).
 __device__ inline void load_to_lds(const int8_t *p, uint32_t lds) {
@@ -162,7 +168,7 @@ __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int BN, int BS, int WN, int WS, int NBUF, bool DIRECT>
+template <int BN, int BS, int WN, int WS, int kBK, int NBUF, bool DIRECT>
 __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
   constexpr int kThr = 64 * WN * WS;
   constexpr int TN = BN / WN / 32, TS = BS / WS / 32;  // 32x32 blocks of a wave
@@ -170,9 +176,9 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   constexpr int kPer = kStage / 16 / kThr;  // chunks a thread moves per stage
   static_assert(kStage % (16 * kThr) == 0, "stage split");
   constexpr int kWide = BN / WN, kLd = kWide + 4;  // a wave's weights, and what a token's sums of them take in LDS
-  constexpr int kTurn = WN * WS * 32 * kLd * 4;
-  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage > kTurn ? NBUF * kStage : kTurn];
-  __shared__ __align__(16) float s_sc[kRows];
+  constexpr int kTurn = WN * WS * 32 * kLd * 4, kEnd = kTurn + kRows * 4;
+  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage > kEnd ? NBUF * kStage : kEnd];
+  float *s_sc = (float *)(s_buf + kTurn);  // after the last stage: the weights' scales, then the tokens'
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wn = wave / WS, wsv = wave % WS;
 
@@ -193,8 +199,9 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   int kc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int p = threadIdx.x + i * kThr, r = p >> 2;
-    kc[i] = ((p & 3) ^ ((r >> 1) & 3)) << 4;
+    constexpr int kC = kBK / 16;  // chunks of a row
+    const int p = threadIdx.x + i * kThr, r = p / kC;
+    kc[i] = ((p % kC) ^ mix_of<kBK>(r)) << 4;
     src[i] = r < BN ? a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw : a.q + (int64_t)min(s0 + r - BN, a.S - 1) * a.ldq;
   }
   const int stages = (a.K + kBK - 1) / kBK;
@@ -212,7 +219,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   // fragment f of a stage's k step: the wave's TN weight blocks, then its TS token blocks
   auto frag = [&](const uint8_t *buf, int f, int kk) {
     const int r = (f < TN ? wn * (BN / WN) + f * 32 : BN + wsv * (BS / WS) + (f - TN) * 32) + row;
-    return *(const i32x4 *)(buf + chunk_of(r, kk * 2 + ck));
+    return *(const i32x4 *)(buf + chunk_of<kBK>(r, kk * 2 + ck));
   };
 
   if constexpr (DIRECT) {
@@ -253,7 +260,9 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
       }
     };
     for (int s = 0; s < stages; ++s) {
-      half(0, s_buf + (s % NBUF) * kStage, 1, -1);
+      const uint8_t *buf = s_buf + (s % NBUF) * kStage;
+#pragma unroll
+      for (int kk = 1; kk < kBK / 32; ++kk) half((kk - 1) & 1, buf, kk, -1);
       wait_loads<(NBUF - 2) * kPer>();
       __builtin_amdgcn_s_barrier();
       half(1, s_buf + ((s + 1) % NBUF) * kStage, 0, s + NBUF);
@@ -278,7 +287,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
       __syncthreads();
       const uint8_t *buf = s_buf + (s % NBUF) * kStage;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < kBK / 32; ++kk) {
         i32x4 A[TN], B[TS];
 #pragma unroll
         for (int i = 0; i < TN; ++i) A[i] = frag(buf, i, kk);
@@ -296,6 +305,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
 
   // Each wave turns its sums round in its own part of the buffers, 32 tokens at a time, so
   // that they leave as runs of a token's neighbouring outputs.
+  __syncthreads();
   for (int i = threadIdx.x; i < kRows; i += kThr)
     s_sc[i] = i < BN ? ldg<float>(a.dw + min(n0 + i, a.N - 1)) : ldg<float>(a.d + min(s0 + i - BN, a.S - 1));
   __syncthreads();
@@ -331,14 +341,14 @@ void launch_few(const QmmArgs &a, hipStream_t st) {
   MOE_LAUNCH((k_qmm_few<MT, NT, W>), g, dim3(64 * W), 0, st, a);
 }
 
-template <int BN, int BS, int WN, int WS, int NBUF>
+template <int BN, int BS, int WN, int WS, int BK, int NBUF>
 void launch_tile(const QmmArgs &a, bool direct, hipStream_t st) {
   const int tn = (a.N + BN - 1) / BN, ts = (a.S + BS - 1) / BS;
   const int64_t total = (int64_t)tn * ts;
   const dim3 g((unsigned)((total + kXcds - 1) / kXcds * kXcds));
   const int group = 4;
-  if (direct) MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, NBUF, true>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
-  else MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, 2, false>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
+  if (direct) MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, BK, NBUF, true>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
+  else MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, 64, 2, false>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
 }
 
 }  // namespace
@@ -353,9 +363,9 @@ hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
   if (a.S <= 16) launch_few<1, 1, 8>(a, st);
   else if (a.S <= 32) launch_few<1, 2, 8>(a, st);
   else if (a.S <= 64) launch_few<1, 4, 8>(a, st);
-  else if ((int64_t)((a.N + 255) / 256) * ((a.S + 255) / 256) >= 192) launch_tile<256, 256, 2, 2, 4>(a, direct, st);
-  else if ((int64_t)((a.N + 127) / 128) * ((a.S + 127) / 128) >= 192) launch_tile<128, 128, 2, 2, 4>(a, direct, st);
-  else launch_tile<64, 64, 2, 2, 4>(a, direct, st);
+  else if ((int64_t)((a.N + 255) / 256) * ((a.S + 255) / 256) >= 192) launch_tile<256, 256, 2, 2, 128, 2>(a, direct, st);
+  else if ((int64_t)((a.N + 127) / 128) * ((a.S + 127) / 128) >= 192) launch_tile<128, 128, 2, 2, 128, 2>(a, direct, st);
+  else launch_tile<64, 64, 2, 2, 128, 3>(a, direct, st);
   return hipGetLastError();
 }
 
