@@ -42,6 +42,14 @@ __device__ inline float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v 
 // fp32 to bf16, round to nearest even.
 __device__ inline uint16_t f_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
+// Two fp32 values as bf16, lo in the low half (one conversion instruction).
+__device__ inline uint32_t pack2_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
 template <bool BF16>
 __device__ inline float load_el(const void *p, int64_t i) {
   if constexpr (BF16) return bf16_f(ldg<uint16_t>((const uint16_t *)p + i));

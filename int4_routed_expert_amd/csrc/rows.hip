@@ -1,6 +1,8 @@
 // Rows in int8 from a norm or a SwiGLU: one pass of arithmetic per element, one scale
 // per row.  norm: v = h / sqrt(mean(h^2) + eps) * gamma with h = t(x + residual);
 // SwiGLU: v = g / (1 + exp(-g)) * u.  Then d = max|v| / 127 and q = rint(v / d).
+#include <algorithm>
+
 #include "dense.h"
 
 namespace moe {
@@ -8,7 +10,22 @@ namespace {
 
 enum RowOp { kNorm, kSilu };
 
-__device__ inline float silu_gate(float g) { return g / (1.0f + expf(-g)); }
+// exp(x) to about 2^-22: 2^t by the hardware (1 ulp) for t = x log2(e) rounded to fp32,
+// times 1 + ln 2 (x log2(e) - t), what the rounding of t dropped.
+__device__ inline float exp_near(float x) {
+  const float hi = 1.44269502f, lo = 1.92596303e-8f;  // log2(e) in two parts
+  const float t = x * hi;
+  const float rest = fmaf(x, lo, fmaf(x, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, rest * 0.693147182f, e);
+}
+
+// silu(g) u.  Below -88 exp would overflow and the quotient vanishes, as the true value
+// nearly does.
+__device__ inline float silu_times(float g, float u) {
+  const float e = g > -88.0f ? exp_near(fmaxf(-g, -126.0f)) : __builtin_inff();
+  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
 
 // v as an int8 code.  The division is IEEE fp32; a denormal scale has too few bits to
 // hold |v / d| at 127, hence the clamp.
@@ -61,7 +78,7 @@ __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
     };
     auto value = [&](int64_t c) {
       if constexpr (OP == kSilu) {
-        return silu_gate(load_el<BF16>(a.x, xr + c)) * load_el<BF16>(a.residual, rr + c);
+        return silu_times(load_el<BF16>(a.x, xr + c), load_el<BF16>(a.residual, rr + c));
       } else {
         const float g = a.g_bf16 ? load_el<true>(a.gamma, c) : load_el<false>(a.gamma, c);
         return (a.h ? load_el<BF16>(a.h, hr + c) : input(c)) * rstd * g;
@@ -95,12 +112,272 @@ __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
   }
 }
 
+// ---- rows held in registers ----------------------------------------------------------
+// A row belongs to W waves and stays in their registers between the passes.  Iteration it
+// of wave w holds the row's block it W + w of 512 elements, 8 a lane: neighbours, moved in
+// 16-byte pieces, where every row is 16-byte aligned (VEC), else 64 apart, so that a wave
+// meets 64 neighbours at a time.
+template <int W, bool VEC>
+__device__ inline int col_of(int tid, int it, int j) {
+  const int block = (it * W + (tid >> 6)) * 512, lane = tid & 63;
+  return VEC ? block + lane * 8 + j : block + j * 64 + lane;
+}
+
+// Eight neighbours of a 16-byte aligned row.
+template <bool BF16>
+__device__ inline void load8(const void *p, int64_t i, float *v) {
+  if constexpr (BF16) {
+    const uint4 r = ldg<uint4>((const uint16_t *)p + i);
+    const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(d[j] << 16);
+      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 r0 = ldg<float4>((const float *)p + i), r1 = ldg<float4>((const float *)p + i + 4);
+    v[0] = r0.x; v[1] = r0.y; v[2] = r0.z; v[3] = r0.w;
+    v[4] = r1.x; v[5] = r1.y; v[6] = r1.z; v[7] = r1.w;
+  }
+}
+template <bool BF16>
+__device__ inline void store8(void *p, int64_t i, const float *v) {
+  if constexpr (BF16) {
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
+    stg<uint4>((uint16_t *)p + i, make_uint4(d[0], d[1], d[2], d[3]));
+  } else {
+    stg<float4>((float *)p + i, make_float4(v[0], v[1], v[2], v[3]));
+    stg<float4>((float *)p + i + 4, make_float4(v[4], v[5], v[6], v[7]));
+  }
+}
+
+// The 8 elements of iteration it, those below H (others are left alone).
+template <int W, bool VEC, bool BF16>
+__device__ inline void load_it(const void *p, int64_t row, int H, int tid, int it, float *v) {
+  const int c = col_of<W, VEC>(tid, it, 0);
+  if (VEC && c + 8 <= H) {
+    load8<BF16>(p, row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = col_of<W, VEC>(tid, it, j);
+      if (k < H) v[j] = load_el<BF16>(p, row + k);
+    }
+  }
+}
+template <int W, bool VEC, bool BF16>
+__device__ inline void store_it(void *p, int64_t row, int H, int tid, int it, const float *v) {
+  const int c = col_of<W, VEC>(tid, it, 0);
+  if (VEC && c + 8 <= H) {
+    store8<BF16>(p, row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = col_of<W, VEC>(tid, it, j);
+      if (k < H) store_el<BF16>(p, row + k, v[j]);
+    }
+  }
+}
+
+// The wave's sum and maximum, in every lane (the row operations leave them in lane 63).
+__device__ inline float wave_sum(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_to63(v)), 63));
+}
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, false));
+}
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0xB1>(v);        // quad_perm [1,0,3,2]
+  v = dpp_max<0x4E>(v);        // quad_perm [2,3,0,1]
+  v = dpp_max<0x141>(v);       // row_half_mirror
+  v = dpp_max<0x140>(v);       // row_mirror
+  v = dpp_max<0x142, 0xA>(v);  // row_bcast:15
+  v = dpp_max<0x143, 0xC>(v);  // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Four values as int8 codes.  In the common range of scales v / d is the product with
+// r = 1 / d and one correction step, which rounds as the division does except next to a
+// midpoint of two fp32 values (three operations in place of about ten); adding 1.5 2^23
+// rounds to the nearest integer, ties to even, and leaves it in the low bits.
+struct Codes {
+  float d, r;
+  bool usable, near;
+  __device__ explicit Codes(float scale) : d(scale) {
+    usable = d > 0.f && d < __builtin_inff();
+    near = d >= 0x1p-100f && d <= 0x1p100f;
+    r = __fdiv_rn(1.0f, d);
+  }
+  __device__ uint32_t one(float v) const {
+    const float p = v * r;
+    return __float_as_uint(fmaf(fmaf(-p, d, v), r, p) + 12582912.0f);
+  }
+  __device__ uint32_t four(const float *v) const {
+    if (near) {
+      const uint32_t lo = __builtin_amdgcn_perm(one(v[1]), one(v[0]), 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(one(v[3]), one(v[2]), 0x04000C0Cu);
+      return lo | hi;
+    }
+    uint32_t w = 0;
+    if (usable) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= ((uint32_t)code_of(v[j], d) & 0xFFu) << (8 * j);
+    }
+    return w;
+  }
+};
+
+template <RowOp OP, bool BF16, int W, int IT, bool VEC>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
+  // each row of a workgroup's turn uses the other half, so one barrier orders both uses
+  __shared__ __align__(16) float s_sum[2][W * IT];
+  __shared__ __align__(16) uint32_t s_max[2][W];
+  constexpr int kRowsAtOnce = W == 1 ? 4 : 1;
+  const int tid = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kRowsAtOnce + (W == 1 ? threadIdx.x >> 6 : 0); r < a.S;
+       r += (int64_t)gridDim.x * kRowsAtOnce, turn ^= 1) {
+    float v[IT][8] = {}, o[IT][8] = {};
+#pragma unroll
+    for (int it = 0; it < IT; ++it) load_it<W, VEC, BF16>(a.x, r * a.ldx, a.H, tid, it, v[it]);
+    if (OP == kSilu || a.residual) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) load_it<W, VEC, BF16>(a.residual, r * a.ldr, a.H, tid, it, o[it]);
+    }
+    if constexpr (OP == kNorm) {
+      // gamma is requested with the row where the registers allow it, else after the sum
+      constexpr bool kEarly = IT == 1;
+      float g[IT][8] = {};
+      auto load_gamma = [&] {
+        if (a.g_bf16) {
+#pragma unroll
+          for (int it = 0; it < IT; ++it) load_it<W, VEC, true>(a.gamma, 0, a.H, tid, it, g[it]);
+        } else {
+#pragma unroll
+          for (int it = 0; it < IT; ++it) load_it<W, VEC, false>(a.gamma, 0, a.H, tid, it, g[it]);
+        }
+      };
+      if constexpr (kEarly) load_gamma();
+      // The squares of a block of 512 are summed by its wave, the blocks in their order:
+      // the same additions for every W and IT, so a row's bits do not depend on the batch.
+      float part[IT];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        part[it] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[it][j] += o[it][j];
+          if constexpr (BF16) v[it][j] = bf16_f(f_bf16(v[it][j]));
+          part[it] = fmaf(v[it][j], v[it][j], part[it]);
+        }
+        part[it] = wave_sum(part[it]);
+        if (a.h) store_it<W, VEC, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it]);
+      }
+      float sum = 0.f;
+      if constexpr (W > 1) {
+        if ((tid & 63) == 0) {
+#pragma unroll
+          for (int it = 0; it < IT; ++it) s_sum[turn][it * W + (tid >> 6)] = part[it];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W * IT; ++i) sum += s_sum[turn][i];
+      } else {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) sum += part[it];
+      }
+      const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+      if constexpr (!kEarly) load_gamma();
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[it][j] = v[it][j] * rstd * g[it][j];
+    } else {
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[it][j] = silu_times(v[it][j], o[it][j]);
+    }
+    if (a.y) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        if (a.y_bf16) store_it<W, VEC, true>(a.y, r * a.ldy, a.H, tid, it, v[it]);
+        else store_it<W, VEC, false>(a.y, r * a.ldy, a.H, tid, it, v[it]);
+      }
+    }
+    if (a.q) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // elements beyond H are 0 (or NaN in a row whose root is not finite, itself NaN)
+          m = max(m, __float_as_uint(v[it][j]) & 0x7FFFFFFFu);
+        }
+      m = wave_max(m);
+      if constexpr (W > 1) {
+        if ((tid & 63) == 0) s_max[turn][tid >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = max(m, s_max[turn][i]);
+      }
+      const Codes c(__fdiv_rn(__uint_as_float(m), 127.0f));
+      if (tid == 0) stg<float>(a.d + r, c.d);
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const uint32_t w[2] = {c.four(v[it]), c.four(v[it] + 4)};
+        const int k = col_of<W, VEC>(tid, it, 0);
+        if (VEC && k + 8 <= a.H) {
+          *(__attribute__((address_space(1))) uint64_t *)(a.q + r * a.ldq + k) = ((uint64_t)w[1] << 32) | w[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int kj = col_of<W, VEC>(tid, it, j);
+            if (kj < a.H) stg<int8_t>(a.q + r * a.ldq + kj, (int8_t)(w[j >> 2] >> (8 * (j & 3))));
+          }
+        }
+      }
+    }
+  }
+}
+
+template <RowOp OP, bool BF16, int W, int IT>
+void launch_one(const RowArgs &a, bool vec, hipStream_t st) {
+  constexpr int kRowsAtOnce = W == 1 ? 4 : 1;
+  const dim3 g((unsigned)std::min<int64_t>(((int64_t)a.S + kRowsAtOnce - 1) / kRowsAtOnce, 1 << 20));
+  const dim3 b(W == 1 ? 256 : 64 * W);
+  if (vec) MOE_LAUNCH((k_rows<OP, BF16, W, IT, true>), g, b, 0, st, a);
+  else MOE_LAUNCH((k_rows<OP, BF16, W, IT, false>), g, b, 0, st, a);
+}
+
+bool on16(const void *p, int64_t ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }
+
+template <RowOp OP, bool BF16>
+void launch_held(const RowArgs &a, hipStream_t st) {
+  const int xs = BF16 ? 2 : 4;
+  const bool vec = on16(a.x, a.ldx, xs) && on16(a.residual, a.ldr, xs) && on16(a.h, a.ldh, xs) &&
+                   on16(a.y, a.ldy, a.y_bf16 ? 2 : 4) && on16(a.gamma, 0, 1) && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0;
+  const bool few = a.S <= 512;  // two rows a compute unit: a row's latency counts
+  if (a.H <= 512) launch_one<OP, BF16, 1, 1>(a, vec, st);
+  else if (a.H <= 1024 && !few) launch_one<OP, BF16, 1, 2>(a, vec, st);
+  else if (a.H <= 2048) few ? launch_one<OP, BF16, 4, 1>(a, vec, st) : launch_one<OP, BF16, 1, 4>(a, vec, st);
+  else if (a.H <= 8192 && few) launch_one<OP, BF16, 16, 1>(a, vec, st);
+  else if (a.H <= 4096) launch_one<OP, BF16, 4, 2>(a, vec, st);
+  else if (a.H <= 6144) launch_one<OP, BF16, OP == kNorm ? 12 : 4, OP == kNorm ? 1 : 3>(a, vec, st);
+  else if (a.H <= 8192) launch_one<OP, BF16, OP == kNorm ? 8 : 4, OP == kNorm ? 2 : 4>(a, vec, st);
+  else if (a.H <= 12288) launch_one<OP, BF16, 12, 2>(a, vec, st);
+  else if (a.H <= 16384) launch_one<OP, BF16, 16, 2>(a, vec, st);
+  else MOE_LAUNCH((k_rows_long<OP, BF16>), dim3((unsigned)std::min(a.S, 1 << 20)), dim3(kRowThreads), 0, st, a);
+}
+
 template <RowOp OP>
 hipError_t launch_rows(const RowArgs &a, int x_bf16, hipStream_t st) {
   ProfScope ps(OP == kNorm ? "norm_quant" : "silu_quant", st);
-  const dim3 g((unsigned)std::min<int64_t>(a.S, 1 << 20)), b(kRowThreads);
-  if (x_bf16) MOE_LAUNCH((k_rows_long<OP, true>), g, b, 0, st, a);
-  else MOE_LAUNCH((k_rows_long<OP, false>), g, b, 0, st, a);
+  if (x_bf16) launch_held<OP, true>(a, st);
+  else launch_held<OP, false>(a, st);
   return hipGetLastError();
 }
 

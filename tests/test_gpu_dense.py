@@ -475,6 +475,20 @@ def test_graph_replays(M, S):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("H", [500, 1000, 2048, 4104, 6144, 8192, 12288, 16384, 20000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_do_not_depend_on_the_batch(M, H, dtype):
+    """A row's bits are the same alone, in a small batch and in a large one."""
+    g = rng(H)
+    x, r = rows(g, 1030, H, dtype), rows(g, 1030, H, dtype)
+    gamma = torch.rand(H, generator=g, device="cuda")
+    many = M.norm_quant(x, gamma, 1e-5, residual=r, y_dtype=BF) + M.silu_quant(x, r, y_dtype=BF)
+    for lo, hi in ((0, 1), (7, 8), (100, 109), (1000, 1030)):
+        few = M.norm_quant(x[lo:hi], gamma, 1e-5, residual=r[lo:hi], y_dtype=BF) + M.silu_quant(x[lo:hi], r[lo:hi], y_dtype=BF)
+        for a, b in zip(many, few):
+            assert torch.equal(a[lo:hi], b)
+
+
 def test_same_rule_as_the_layers_int8_activations(M):
     """The norm's int8 rows are what moe_cfg.act_int8 makes of the same fp32 rows: d = max|v| / 127, q = rint(v / d)."""
     x = rows(rng(1), 50, 1024, F32)
