@@ -1,36 +1,181 @@
 // Rotary positions: pair i of a head turns by a = pos * freqs[i].
 //   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+//
+// Bound by memory: every element is read and written once.  A workgroup takes a few
+// tokens (a part of one token's heads where there are few tokens), forms their sines and
+// cosines once in LDS, a pair a thread, and streams the heads in units of 16 bytes per
+// half pair.
+#include <algorithm>
+
 #include "dense.h"
 
 namespace moe {
 namespace {
 
-// One thread per (token, head, pair); its threads also copy what lies outside the part.
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_rope_pairs(RopeArgs a, int interleaved) {
-  for (int64_t s = blockIdx.x; s < a.S; s += gridDim.x) {
-    const double pos = a.pos_i64 ? (double)((const int64_t *)a.pos)[s] : (double)((const int32_t *)a.pos)[s];
-    for (int ti = 0; ti < 2; ++ti) {
-      const moe_rope_tensor &t = a.t[ti];
-      for (int u = threadIdx.x; u < t.heads * a.half; u += blockDim.x) {
-        const int hd = u / a.half, i = u - hd * a.half;
-        const int c1 = a.offset + (interleaved ? 2 * i : i), c2 = interleaved ? c1 + 1 : c1 + a.half;
-        const int64_t in = s * t.x_token + hd * t.x_head, out = s * t.out_token + hd * t.out_head;
-        const double w = pos * a.freqs[i];
-        const float c = a.factor * (float)cos(w), sn = a.factor * (float)sin(w);
-        const float x1 = load_el<BF16>(t.x, in + c1), x2 = load_el<BF16>(t.x, in + c2);
-        store_el<BF16>(t.out, out + c1, x1 * c - x2 * sn);
-        store_el<BF16>(t.out, out + c2, x2 * c + x1 * sn);
-      }
-      const int rest = a.D - 2 * a.half;
-      if (t.x != t.out)
-        for (int u = threadIdx.x; u < t.heads * rest; u += blockDim.x) {
-          const int hd = u / rest, i = u - hd * rest;
-          const int c = i < a.offset ? i : i + 2 * a.half;
-          store_el<BF16>(t.out, s * t.out_token + hd * t.out_head + c,
-                         load_el<BF16>(t.x, s * t.x_token + hd * t.x_head + c));
-        }
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAngles = 1024;  // angles a workgroup may hold (8 KB of LDS)
+
+// Cosine and sine of pos * f, each within about 2^-24 of the true value for any position:
+// quarter turns are taken off in fp64, so the rest r, |r| <= pi / 4, is exact to the last
+// bit of fp32, where the Taylor series to r^9 and r^8 leave less than 2^-25.
+__device__ inline float2 cos_sin(double pos, double f) {
+  const double turns = pos * f * 0.63661977236758134308;  // 2 / pi
+  const double n = rint(turns);
+  const float r = (float)((turns - n) * 1.57079632679489661923);
+  const int quarter = (int)(int64_t)n & 3;
+  const float r2 = r * r;
+  const float s = fmaf(r * r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), r);
+  const float c = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+  return make_float2(quarter == 1 || quarter == 2 ? -cc : cc, quarter >= 2 ? -ss : ss);
+}
+
+// V neighbouring elements as floats (V 1, or 16 bytes' worth).
+template <bool BF16, int V>
+__device__ inline void load_v(const void *p, int64_t i, float *v) {
+  if constexpr (V == 1) {
+    v[0] = load_el<BF16>(p, i);
+  } else if constexpr (BF16) {
+    const uint4 r = ldg<uint4>((const uint16_t *)p + i);
+    const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(d[j] << 16);
+      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
     }
+  } else {
+    const float4 r = ldg<float4>((const float *)p + i);
+    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+  }
+}
+template <bool BF16, int V>
+__device__ inline void store_v(void *p, int64_t i, const float *v) {
+  if constexpr (V == 1) {
+    store_el<BF16>(p, i, v[0]);
+  } else if constexpr (BF16) {
+    stg<uint4>((uint16_t *)p + i, make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]),
+                                             pack2_bf16(v[6], v[7])));
+  } else {
+    stg<float4>((float *)p + i, make_float4(v[0], v[1], v[2], v[3]));
+  }
+}
+
+// n / d for n < 2^20, d < 2^11 as a product: m = ceil(2^32 / d) is less than 1 too large a
+// factor per n, so floor(n m / 2^32) is the quotient while n d < 2^32.
+__device__ inline int quot(int n, uint32_t m, int d) { return d == 1 ? n : (int)__umulhi((uint32_t)n, m); }
+
+struct RopePlan {
+  int tokens;     // tokens of a workgroup
+  int parts;      // workgroups that share a token's heads (1 where tokens > 1)
+  int units;      // units of one head: turning ones first, then those that are only copied
+  int turning;
+  uint32_t m_units, m_token;
+};
+
+// A turning unit: V pairs (half layout: V elements of each half; interleaved: V elements
+// from each of two neighbouring runs, or one pair where V = 1).  A copied unit: V elements.
+template <bool BF16, int V, bool INTER>
+__global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, RopePlan p) {
+  __shared__ float2 s_cs[kRopeAngles];
+  const int64_t s0 = (int64_t)(blockIdx.x / p.parts) * p.tokens;
+  const int part = blockIdx.x % p.parts;
+  const int tokens = (int)min((int64_t)p.tokens, a.S - s0);
+  for (int i = threadIdx.x; i < tokens * a.half; i += kRopeThreads) {
+    const int t = i / a.half, k = i - t * a.half;
+    const double pos = a.pos_i64 ? (double)ldg<int64_t>((const int64_t *)a.pos + s0 + t)
+                                 : (double)ldg<int32_t>((const int32_t *)a.pos + s0 + t);
+    const float2 cs = cos_sin(pos, ldg<double>(a.freqs + k));
+    s_cs[i] = make_float2(cs.x * a.factor, cs.y * a.factor);
+  }
+  __syncthreads();
+  const int heads = a.t[0].heads + a.t[1].heads;
+  const int per_token = heads * p.units, total = tokens * per_token;
+  for (int u = threadIdx.x + part * kRopeThreads; u < total; u += p.parts * kRopeThreads) {
+    const int t = p.tokens == 1 ? 0 : quot(u, p.m_token, per_token);
+    const int w = u - t * per_token, hd = quot(w, p.m_units, p.units), e = w - hd * p.units;
+    const bool second = hd >= a.t[0].heads;
+    const int h = second ? hd - a.t[0].heads : hd;
+    const int64_t s = s0 + t;
+    const void *x = second ? a.t[1].x : a.t[0].x;
+    void *out = second ? a.t[1].out : a.t[0].out;
+    const int64_t in = s * (second ? a.t[1].x_token : a.t[0].x_token) + h * (second ? a.t[1].x_head : a.t[0].x_head);
+    const int64_t to = s * (second ? a.t[1].out_token : a.t[0].out_token) + h * (second ? a.t[1].out_head : a.t[0].out_head);
+    if (e >= p.turning) {
+      if (x == out) continue;
+      int c = (e - p.turning) * V;
+      if (c >= a.offset) c += 2 * a.half;
+      float v[V];
+      load_v<BF16, V>(x, in + c, v);
+      store_v<BF16, V>(out, to + c, v);
+      continue;
+    }
+    const int i0 = e * V;  // the unit's first pair
+    const int c1 = a.offset + (INTER ? 2 * i0 : i0), c2 = INTER ? c1 + V : c1 + a.half;
+    float v1[V], v2[V], w1[V], w2[V];
+    load_v<BF16, V>(x, in + c1, v1);
+    load_v<BF16, V>(x, in + c2, v2);
+    const float2 *cs = s_cs + t * a.half + i0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float2 k = cs[j];
+      // pair j's elements: half layout v1[j], v2[j]; interleaved elements 2j and 2j + 1 of v1 v2
+      const float x1 = INTER && V > 1 ? (2 * j < V ? v1[(2 * j) % V] : v2[(2 * j) % V]) : v1[j];
+      const float x2 = INTER && V > 1 ? (2 * j < V ? v1[(2 * j + 1) % V] : v2[(2 * j + 1) % V]) : v2[j];
+      // written as fused operations, so that both unit sizes give the same bits
+      const float y1 = fmaf(x1, k.x, -(x2 * k.y)), y2 = fmaf(x2, k.x, x1 * k.y);
+      if (INTER && V > 1) {
+        if (2 * j < V) { w1[(2 * j) % V] = y1; w1[(2 * j + 1) % V] = y2; }
+        else { w2[(2 * j) % V] = y1; w2[(2 * j + 1) % V] = y2; }
+      } else {
+        w1[j] = y1;
+        w2[j] = y2;
+      }
+    }
+    store_v<BF16, V>(out, to + c1, w1);
+    store_v<BF16, V>(out, to + c2, w2);
+  }
+}
+
+template <bool BF16, bool INTER>
+void launch(const RopeArgs &a, hipStream_t st) {
+  constexpr int kV = BF16 ? 8 : 4;
+  // 16-byte units: every stride and the part's place in a head are multiples of them
+  bool vec = a.D % kV == 0 && a.offset % kV == 0 && a.half % kV == 0;
+  for (const auto &t : a.t)
+    if (t.heads)
+      vec = vec && (uintptr_t)t.x % 16 == 0 && (uintptr_t)t.out % 16 == 0 && t.x_token % kV == 0 && t.x_head % kV == 0 &&
+            t.out_token % kV == 0 && t.out_head % kV == 0;
+  const int V = vec ? kV : 1;
+  RopePlan p{};
+  p.turning = a.half / V;
+  p.units = p.turning + (a.D - 2 * a.half) / V;
+  const int per_token = (a.t[0].heads + a.t[1].heads) * p.units;
+  // Tokens until a workgroup's threads all have a unit, while the angles fit and every
+  // compute unit still has a few workgroups; a token shared between workgroups where
+  // there are fewer tokens than that.
+  p.tokens = std::max(1, std::min({kRopeThreads / per_token, kRopeAngles / a.half, a.S / 1024}));
+  p.parts = std::max(1, std::min((per_token + kRopeThreads - 1) / kRopeThreads, 1024 / a.S));
+  if (p.tokens > 1) p.parts = 1;
+  auto magic = [](int d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u; };
+  p.m_units = magic(p.units);
+  p.m_token = magic(per_token);
+  const int64_t blocks = ((int64_t)a.S + p.tokens - 1) / p.tokens * p.parts;
+  const dim3 b(kRopeThreads);
+  // a launch holds fewer than 2^32 threads: longer inputs go in pieces
+  const int64_t most = (int64_t)(1 << 20);
+  for (int64_t at = 0; at < blocks; at += most) {
+    RopeArgs c = a;
+    const int64_t s = at / p.parts * p.tokens;
+    c.S = (int)(a.S - s);
+    c.pos = (const char *)a.pos + s * (a.pos_i64 ? 8 : 4);
+    for (auto &t : c.t)
+      if (t.heads) {
+        t.x = (const char *)t.x + s * t.x_token * (BF16 ? 2 : 4);
+        t.out = (char *)t.out + s * t.out_token * (BF16 ? 2 : 4);
+      }
+    const dim3 g((unsigned)std::min(blocks - at, most));
+    if (vec) MOE_LAUNCH((k_rope<BF16, kV, INTER>), g, b, 0, st, c, p);
+    else MOE_LAUNCH((k_rope<BF16, 1, INTER>), g, b, 0, st, c, p);
   }
 }
 
@@ -38,9 +183,8 @@ __global__ __launch_bounds__(256) void k_rope_pairs(RopeArgs a, int interleaved)
 
 hipError_t launch_rope(const RopeArgs &a, int x_bf16, int interleaved, hipStream_t st) {
   ProfScope ps("rope", st);
-  const dim3 g((unsigned)std::min(a.S, 1 << 20)), b(256);
-  if (x_bf16) MOE_LAUNCH(k_rope_pairs<true>, g, b, 0, st, a, interleaved);
-  else MOE_LAUNCH(k_rope_pairs<false>, g, b, 0, st, a, interleaved);
+  if (x_bf16) interleaved ? launch<true, true>(a, st) : launch<true, false>(a, st);
+  else interleaved ? launch<false, true>(a, st) : launch<false, false>(a, st);
   return hipGetLastError();
 }
 
