@@ -11,6 +11,8 @@ import ctypes
 import os
 import re
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
@@ -324,6 +326,10 @@ def moe_chain_destroy(chain: int | None) -> None:
     _lib.moe_chain_destroy(chain)
 
 
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_ROWS = torch.contiguous_format
+
+
 # ---- dense operators ---------------------------------------------------------------------------------------------------
 
 def moe_norm_quant(x, x_dtype: int, ldx: int, residual, ldr: int, gamma, g_dtype: int, eps: float, S: int, H: int, h,
@@ -366,21 +372,20 @@ def moe_rope_freqs(rot: int, theta: float, scaling: int, scale: float, trained_l
 
 
 def _code(dtype, what: str) -> int:
-    import torch
-    if dtype == torch.bfloat16:
-        return MOE_BF16
-    if dtype == torch.float32:
-        return MOE_F32
-    raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"{what} must be float32 or bfloat16, not {dtype}")
+    return code
 
 
 def _rows(t, shape, what: str) -> int:
-    """Row stride of the matrix t, whose rows must be contiguous (and, when shape is given, whose shape it must be)."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape) or (t.shape[1] > 1 and t.stride(1) != 1):
-        want = "" if shape is None else f" of shape {list(shape)}"
-        raise ValueError(f"{what} must be a matrix{want} with contiguous rows, not {tuple(t.shape)} "
-                         f"with strides {tuple(t.stride())}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """Row stride of the matrix t, whose rows must be contiguous and whose shape must be `shape`."""
+    if t.shape == shape and len(shape) == 2:
+        row, col = t.stride()
+        if col == 1 or shape[1] <= 1:
+            return row if shape[0] > 1 else shape[1]
+    raise ValueError(f"{what} must be a matrix with contiguous rows, of shape {tuple(shape)}, not {tuple(t.shape)} "
+                     f"with strides {tuple(t.stride())}")
 
 
 def _vector(t, n: int, dtype, what: str) -> None:
@@ -388,107 +393,121 @@ def _vector(t, n: int, dtype, what: str) -> None:
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}, not {tuple(t.shape)} {t.dtype}")
 
 
-def _one_device(first, *others):
-    """The GPU that every given tensor is on."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors must be on a GPU, not on {dev}")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"the tensors must be on one GPU, not on {dev} and {t.device}")
-    return dev
+# The handle of a GPU's current stream.  Small calls are bound by this module's own time: the handle alone, where torch
+# has it, comes twenty times as fast as a stream object.
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-class _launch:
-    """Where a call that allocates its outputs launches: the tensors' GPU and the stream asked for (None: that GPU's
-    current one) become current, so that the outputs belong to the stream that writes them, and the inputs are kept
-    from reuse by their own streams until it is done with them."""
+def _gpu(*tensors) -> int:
+    """The index of the GPU that every given tensor is on."""
+    i = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"the tensors must be on one GPU, not on {tensors[0].device} and {t.device}")
+    if i < 0:
+        raise ValueError(f"the tensors must be on a GPU, not on {tensors[0].device}")
+    return i
 
-    def __init__(self, dev, stream, *inputs):
-        import torch
-        self.contexts = []
-        if dev.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(dev))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            self.contexts.append(torch.cuda.stream(stream))
+
+def _elsewhere(gpu: int, stream, f, inputs, *args, **kw):
+    """f(*args, **kw) with `gpu`, and `stream` where one is given, made current: the outputs that f allocates then belong
+    to the stream that writes them, and the memory of its inputs is not given out again before that stream is done."""
+    with torch.cuda.device(gpu):
+        if stream is None:
+            return f(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
             for t in inputs:
                 if t is not None:
                     t.record_stream(stream)
-        self.dev = dev
-
-    def __enter__(self):
-        import torch
-        for c in self.contexts:
-            c.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *error):
-        for c in reversed(self.contexts):
-            c.__exit__(*error)
+            return f(*args, **kw)
 
 
 def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant: bool = True, stream=None):
     """(h, y, q, d) of the rows x [S, H]: moe_norm_quant with its outputs allocated on x's GPU.  h is the residual
     sum (None without a residual; written over the tensor given as h, which may be residual or x), y the norm in
     y_dtype (None: not wanted), q int8 and d fp32 the norm's quantised rows (None with quant=False)."""
-    import torch
-    xd, gd = _code(x.dtype, "x"), _code(gamma.dtype, "gamma")
-    ldx = _rows(x, None, "x")
-    S, H = x.shape
+    dtype, shape = x.dtype, x.shape
+    xd, gd = _code(dtype, "x"), _code(gamma.dtype, "gamma")
+    ldx = _rows(x, shape, "x")
+    S, H = shape
     _vector(gamma, H, gamma.dtype, "gamma")
-    ldr = ldh = ldy = 0
+    ldr = ldh = ldy = ldq = yd = 0
     if residual is not None:
-        ldr = _rows(residual, (S, H), "residual")
-        if residual.dtype != x.dtype:
-            raise ValueError(f"residual must have x's type {x.dtype}, not {residual.dtype}")
+        ldr = _rows(residual, shape, "residual")
+        if residual.dtype != dtype:
+            raise ValueError(f"residual must have x's type {dtype}, not {residual.dtype}")
     if h is not None:
         if residual is None:
             raise ValueError("h is the sum with a residual: none is given")
-        ldh = _rows(h, (S, H), "h")
-        if h.dtype != x.dtype:
-            raise ValueError(f"h must have x's type {x.dtype}, not {h.dtype}")
-    yd = MOE_F32 if y_dtype is None else _code(y_dtype, "y_dtype")
-    if residual is None and y_dtype is None and not quant:
+        ldh = _rows(h, shape, "h")
+        if h.dtype != dtype:
+            raise ValueError(f"h must have x's type {dtype}, not {h.dtype}")
+    if y_dtype is not None:
+        yd = _code(y_dtype, "y_dtype")
+    elif residual is None and not quant:
         raise ValueError("no output is asked for")
-    dev = _one_device(x, gamma, residual, h)
-    with _launch(dev, stream, x, gamma, residual, h) as st:
-        if residual is not None and h is None:
-            h, ldh = torch.empty((S, H), dtype=x.dtype, device=dev), H
-        y = torch.empty((S, H), dtype=y_dtype, device=dev) if y_dtype is not None else None
-        q = torch.empty((S, H), dtype=torch.int8, device=dev) if quant else None
-        d = torch.empty(S, dtype=torch.float32, device=dev) if quant else None
-        moe_norm_quant(x, xd, ldx, residual, ldr, gamma, gd, eps, S, H, h, ldh, y, yd, H, q, H, d, st)
+    gpu = _gpu(x, gamma, residual, h)
+    if stream is not None or gpu != torch.cuda.current_device():
+        return _elsewhere(gpu, stream, norm_quant, (x, gamma, residual, h), x, gamma, eps, residual, h, y_dtype, quant)
+    y = q = d = None
+    py = pq = pd = ph = pr = None
+    if residual is not None:
+        pr = residual.data_ptr()
+        if h is None:
+            h = torch.empty_like(x, memory_format=_ROWS)
+            ldh = H
+        ph = h.data_ptr()
+    if y_dtype is not None:
+        y = torch.empty_like(x, dtype=y_dtype, memory_format=_ROWS)
+        py = y.data_ptr()
+    if quant:
+        q, d = torch.empty_like(x, dtype=torch.int8, memory_format=_ROWS), x.new_empty(S, dtype=torch.float32)
+        pq, pd = q.data_ptr(), d.data_ptr()
+    rc = _lib.moe_norm_quant(x.data_ptr(), xd, ldx, pr, ldr, gamma.data_ptr(), gd, eps, S, H, ph, ldh, py, yd, H, pq, H, pd,
+                             _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_norm_quant")
     return h, y, q, d
 
 
 def silu_quant(g, u=None, y_dtype=None, quant: bool = True, stream=None):
     """(y, q, d) of silu(g) * u, both [S, I], or of the halves of g [S, 2 I] where u is None: moe_silu_quant with its
     outputs allocated on g's GPU.  y in y_dtype (None: not wanted), q int8 and d fp32 (None with quant=False)."""
-    import torch
-    xd, ldx = _code(g.dtype, "g"), _rows(g, None, "g")
-    S, I = g.shape
+    dtype, shape = g.dtype, g.shape
+    xd, ldx = _code(dtype, "g"), _rows(g, shape, "g")
+    S, I = shape
+    up = g.data_ptr()
     if u is None:
         if I % 2:
             raise ValueError(f"g holds gate and up side by side: its width {I} must be even")
         I //= 2
-        up = ptr(g) + I * g.element_size() if S else None
+        up += I * g.element_size()
     else:
-        if u.dtype != g.dtype:
-            raise ValueError(f"u must have g's type {g.dtype}, not {u.dtype}")
-        if _rows(u, (S, I), "u") != ldx:
+        if u.dtype != dtype:
+            raise ValueError(f"u must have g's type {dtype}, not {u.dtype}")
+        if _rows(u, shape, "u") != ldx:
             raise ValueError(f"u must have g's row stride {ldx}, not {u.stride(0)}")
-        up = ptr(u)
-    yd = MOE_F32 if y_dtype is None else _code(y_dtype, "y_dtype")
-    if y_dtype is None and not quant:
+        up = u.data_ptr()
+    yd = 0
+    if y_dtype is not None:
+        yd = _code(y_dtype, "y_dtype")
+    elif not quant:
         raise ValueError("no output is asked for")
-    dev = _one_device(g, u)
-    with _launch(dev, stream, g, u) as st:
-        y = torch.empty((S, I), dtype=y_dtype, device=dev) if y_dtype is not None else None
-        q = torch.empty((S, I), dtype=torch.int8, device=dev) if quant else None
-        d = torch.empty(S, dtype=torch.float32, device=dev) if quant else None
-        moe_silu_quant(g, up, xd, ldx, S, I, y, yd, I, q, I, d, st)
+    gpu = _gpu(g, u)
+    if stream is not None or gpu != torch.cuda.current_device():
+        return _elsewhere(gpu, stream, silu_quant, (g, u), g, u, y_dtype, quant)
+    y = q = d = py = pq = pd = None
+    if y_dtype is not None:
+        y = g.new_empty((S, I), dtype=y_dtype)
+        py = y.data_ptr()
+    if quant:
+        q, d = g.new_empty((S, I), dtype=torch.int8), g.new_empty(S, dtype=torch.float32)
+        pq, pd = q.data_ptr(), d.data_ptr()
+    rc = _lib.moe_silu_quant(g.data_ptr(), up, xd, ldx, S, I, py, yd, I, pq, I, pd, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_silu_quant")
     return y, q, d
 
 
@@ -496,28 +515,29 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
     """y [S, N] in out_dtype (bfloat16 unless given): moe_qmatmul of the int8 rows q [S, K] with scales d [S] and the
     int8 weights w [N, K] with scales dw [N], with its output (and, when ws is None, a workspace) allocated on q's
     GPU."""
-    import torch
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    out_dtype = out_dtype or torch.bfloat16
     yd = _code(out_dtype, "out_dtype")
-    ldq = _rows(q, None, "q")
-    S, K = q.shape
-    if w.dim() != 2:
-        raise ValueError(f"w must be a matrix, not {tuple(w.shape)}")
-    N = w.shape[0]
+    shape = q.shape
+    ldq = _rows(q, shape, "q")
+    S, K = shape
+    N = w.shape[0] if w.dim() else 0
     ldw = _rows(w, (N, K), "w")
     if q.dtype != torch.int8 or w.dtype != torch.int8:
         raise ValueError(f"q and w must be int8, not {q.dtype} and {w.dtype}")
     _vector(d, S, torch.float32, "d")
     _vector(dw, N, torch.float32, "dw")
-    dev = _one_device(q, d, w, dw, ws)
-    need = moe_qmatmul_workspace_bytes(S, N, K)
-    if need < 0:
-        raise MoeError(need, "moe_qmatmul")
-    with _launch(dev, stream, q, d, w, dw, ws) as st:
-        if need and ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        y = torch.empty((S, N), dtype=out_dtype, device=dev)
-        moe_qmatmul(q, ldq, d, w, ldw, dw, S, N, K, y, yd, N, ws, ws.numel() * ws.element_size() if need else 0, st)
+    gpu = _gpu(q, d, w, dw, ws)
+    if stream is not None or gpu != torch.cuda.current_device():
+        return _elsewhere(gpu, stream, qmatmul, (q, d, w, dw, ws), q, d, w, dw, out_dtype, ws)
+    need = _lib.moe_qmatmul_workspace_bytes(S, N, K)
+    if need > 0 and ws is None:
+        ws = q.new_empty(need)
+    y = d.new_empty((S, N), dtype=out_dtype)
+    rc = _lib.moe_qmatmul(q.data_ptr(), ldq, d.data_ptr(), w.data_ptr(), ldw, dw.data_ptr(), S, N, K, y.data_ptr(), yd, N,
+                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+                          _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_qmatmul")
     return y
 
 
@@ -534,48 +554,48 @@ def rope_freqs(rot: int, theta: float = 10000.0, scaling: str = "none", scale: f
     return torch.from_numpy(f).to(device), factor
 
 
-def _heads(t, S: int, D: int, what: str) -> None:
-    if t.dim() != 3 or t.shape[0] != S or t.shape[2] != D or (D > 1 and t.stride(2) != 1):
-        raise ValueError(f"{what} must be [{S}, heads, {D}] with contiguous heads, not {tuple(t.shape)} "
-                         f"with strides {tuple(t.stride())}")
+def _heads(t, S: int, D: int, what: str):
+    if t.dim() == 3 and t.shape[0] == S and t.shape[2] == D and t.stride(2) == 1:
+        return t.stride()
+    raise ValueError(f"{what} must be [{S}, heads, {D}] with contiguous heads, not {tuple(t.shape)} "
+                     f"with strides {tuple(t.stride())}")
 
 
 def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: float = 1.0, inplace: bool = False,
          stream=None):
     """(q, k) turned to their positions: moe_rope of q [S, heads, D] and k [S, kheads, D] (or None), with pos [S] int32
     or int64 and freqs [rot / 2] float64, into tensors allocated on q's GPU, or over q and k with inplace=True."""
-    import torch
-    xd = _code(q.dtype, "q")
+    dtype = q.dtype
+    xd = _code(dtype, "q")
     S, D = q.shape[0], q.shape[-1]
-    _heads(q, S, D, "q")
+    strides = [_heads(q, S, D, "q"), None]
     if k is not None:
-        _heads(k, S, D, "k")
-        if k.dtype != q.dtype:
-            raise ValueError(f"k must have q's type {q.dtype}, not {k.dtype}")
-    if pos.dtype not in (torch.int32, torch.int64):
+        strides[1] = _heads(k, S, D, "k")
+        if k.dtype != dtype:
+            raise ValueError(f"k must have q's type {dtype}, not {k.dtype}")
+    wide = pos.dtype == torch.int64
+    if not wide and pos.dtype != torch.int32:
         raise ValueError(f"pos must be int32 or int64, not {pos.dtype}")
     _vector(pos, S, pos.dtype, "pos")
-    if freqs.dim() != 1:
-        raise ValueError(f"freqs must be a vector, not {tuple(freqs.shape)}")
-    _vector(freqs, freqs.shape[0], torch.float64, "freqs")
-    dev = _one_device(q, k, pos, freqs)
-    with _launch(dev, stream, q, k, pos, freqs) as st:
-        outs, args = [], []
-        for t in (q, k):
-            if t is None or t.shape[1] == 0:
-                outs.append(t)
-                args.append(None)
-                continue
-            o = t if inplace else torch.empty(t.shape, dtype=t.dtype, device=dev)
-            outs.append(o)
-            s0, s1, _ = t.stride()
-            o0, o1 = (s0, s1) if inplace else (t.shape[1] * D, D)
-            args.append(moe_rope_tensor(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, t.shape[1]))
-        if args[0] is None:
-            raise ValueError("q has no heads")
-        moe_rope(args[0], args[1], xd, S, D, 2 * freqs.shape[0], offset,
-                 MOE_ROPE_INTERLEAVED if interleaved else MOE_ROPE_HALF, pos, int(pos.dtype == torch.int64), freqs,
-                 factor, st)
+    half = freqs.shape[0] if freqs.dim() == 1 else -1
+    _vector(freqs, half, torch.float64, "freqs")
+    gpu = _gpu(q, k, pos, freqs)
+    if stream is not None or gpu != torch.cuda.current_device():
+        return _elsewhere(gpu, stream, rope, (q, k, pos, freqs), q, k, pos, freqs, offset, interleaved, factor, inplace)
+    outs, args = [q, k], [None, None]
+    for i, t in enumerate((q, k)):
+        if t is None:
+            continue
+        o = outs[i] = t if inplace else torch.empty_like(t, memory_format=_ROWS)
+        s0, s1, _ = strides[i]
+        heads = t.shape[1]
+        o0, o1 = (s0, s1) if inplace else (heads * D, D)
+        args[i] = ctypes.byref(moe_rope_tensor(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, heads))
+    rc = _lib.moe_rope(args[0], args[1], xd, S, D, 2 * half, offset,
+                       MOE_ROPE_INTERLEAVED if interleaved else MOE_ROPE_HALF, pos.data_ptr(), wide, freqs.data_ptr(), factor,
+                       _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_rope")
     return outs[0], outs[1]
 
 
