@@ -157,9 +157,10 @@ __device__ inline int chunk_of(int r, int c) {
   return r * BK + ((c ^ mix_of<BK>(r)) << 4);
 }
 
-// One 16-byte load per lane from p straight into LDS, to lds + 16 lane (lds wave-uniform).
-__device__ inline void load_to_lds(const int8_t *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(p) : "memory");
+// One 16-byte load per lane from p straight into LDS, to lds + off + 16 lane (lds
+// wave-uniform, off a constant).
+__device__ inline __attribute__((always_inline)) void load_to_lds(const int8_t *p, uint32_t lds, int off) {
+  asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p), "i"(off) : "memory", "scc");
 }
 
 // Waits until at most N of this wave's loads are in flight and its reads of LDS are done.
@@ -216,57 +217,100 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
   const int row = lane & 31, ck = lane >> 5;
-  // fragment f of a stage's k step: the wave's TN weight blocks, then its TS token blocks
-  auto frag = [&](const uint8_t *buf, int f, int kk) {
-    const int r = (f < TN ? wn * (BN / WN) + f * 32 : BN + wsv * (BS / WS) + (f - TN) * 32) + row;
-    return *(const i32x4 *)(buf + chunk_of<kBK>(r, kk * 2 + ck));
+  // where this lane finds its 16 bytes of k step kk in the wave's first weight and token
+  // blocks (32 rows further on they lie 32 kBK bytes further: chunks are mixed over 16 rows)
+  constexpr int kSteps = kBK / 32;
+  int at_w[kSteps], at_t[kSteps];
+#pragma unroll
+  for (int kk = 0; kk < kSteps; ++kk) {
+    at_w[kk] = chunk_of<kBK>(wn * (BN / WN) + row, kk * 2 + ck);
+    at_t[kk] = chunk_of<kBK>(BN + wsv * (BS / WS) + row, kk * 2 + ck);
+  }
+  // fragment f of a k step: the wave's TN weight blocks, then its TS token blocks
+  auto frag = [&](const uint8_t *buf, int f, int kk) __attribute__((always_inline)) {
+    return *(const i32x4 *)(buf + (f < TN ? at_w[kk] + f * 32 * kBK : at_t[kk] + (f - TN) * 32 * kBK));
   };
 
   if constexpr (DIRECT) {
     // The wait for a stage leaves the requests of the stages after it in flight, so the
     // requests are written in assembly: a load into LDS known to the compiler makes it
-    // wait for all of them before the next read of LDS.  Beyond K a request reads zeros.
+    // wait for all of them before the next read of LDS.  A wave issues one instruction in
+    // about four cycles, so what surrounds the MFMAs is kept short: the sources advance by
+    // a stage, and only near the end of K are chunks beyond it pointed at zeros.
     constexpr int kF = TN + TS, kM = TN * TS;
-    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024;
-    auto request = [&](int i, int s) {
-      const int8_t *p = src[i] + (int64_t)s * kBK + kc[i];
-      if (s >= whole && (int64_t)s * kBK + kc[i] >= a.K) p = (const int8_t *)g_zeros;
-      load_to_lds(p, lds + (s % NBUF) * kStage + i * kThr * 16);
+    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
+        (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) src[i] += kc[i];
+    auto clip = [&](int s) __attribute__((always_inline)) {  // before stage s is requested
+      if (s >= whole) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if ((int64_t)s * kBK + kc[i] >= a.K) src[i] = (const int8_t *)g_zeros;
+      }
     };
-    for (int s = 0; s < NBUF; ++s)
+    auto request = [&](int i, int buffer) __attribute__((always_inline)) {
+      load_to_lds(src[i], lds, buffer * kStage + i * kThr * 16);
+      src[i] += kBK;
+    };
+#pragma unroll
+    for (int s = 0; s < NBUF; ++s) {
+      clip(s);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) request(i, s);
-    wait_loads<(NBUF - 1) * kPer>();
+    }
+    wait_loads<0>();
     __builtin_amdgcn_s_barrier();
-    i32x4 F[2][kF];
+    // Fragments are read a group of kG k steps ahead, at least 4 MFMAs: they take longer to
+    // arrive than one MFMA takes.
+    constexpr int kG = kM >= 4 ? (kM >= 8 ? 1 : 2) : kSteps < 4 ? kSteps : 4, kGroups = kSteps / kG;
+    static_assert(kSteps % kG == 0 && NBUF % 2 == 0, "groups of k steps");
+    i32x4 F[2][kG][kF];
 #pragma unroll
-    for (int f = 0; f < kF; ++f) F[0][f] = frag(s_buf, f, 0);
-    // Half a stage: multiply one k step's fragments while the next step's are read and,
-    // in the second half, the stage just read is requested anew, spread between the MFMAs.
-    auto half = [&](int cur, const uint8_t *buf, int kk, int again) {
+    for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
+    // Multiply one group's fragments while the next group's are read and, in a stage's last
+    // group, the stage just read is requested anew, spread between the MFMAs.
+    auto multiply = [&](int cur, int buffer, int g, int again, int r0, int r1) __attribute__((always_inline)) {
+      constexpr int kAll = kG * kM;
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
+      for (int m = 0; m < kAll; ++m) {
 #pragma unroll
-        for (int f = 0; f < kF; ++f)
-          if (f * kM / kF == m) F[cur ^ 1][f] = frag(buf, f, kk);
-        if (again >= 0) {
+        for (int f = 0; f < kG * kF; ++f)
+          if (f * kAll / (kG * kF) == m) F[cur ^ 1][f / kF][f % kF] = frag(s_buf + buffer * kStage, f % kF, g * kG + f / kF);
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (i * kM / kPer == m) request(i, again);
-        }
-        acc[m / TS][m % TS] =
-            __builtin_amdgcn_mfma_i32_32x32x32_i8(F[cur][m / TS], F[cur][TN + m % TS], acc[m / TS][m % TS], 0, 0, 0);
+        for (int i = 0; i < kPer; ++i)
+          if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
+        const int k = m / kM, i = m % kM / TS, j = m % TS;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F[cur][k][i], F[cur][k][TN + j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (int s = 0; s < stages; ++s) {
-      const uint8_t *buf = s_buf + (s % NBUF) * kStage;
+    // A stage's new requests go out over its own last group and the first of the next stage:
+    // all in one group they wait for each other (8192x12288x6144: 582 us, 558 over two, 571
+    // over four, where the last arrive late).
+    constexpr int kSpread = kGroups > 1 ? 2 : 1;
+    auto stage = [&](int s, int b) __attribute__((always_inline)) {  // stage s, in buffer b
+      const int cur = b * kGroups & 1;
 #pragma unroll
-      for (int kk = 1; kk < kBK / 32; ++kk) half((kk - 1) & 1, buf, kk, -1);
+      for (int g = 1; g < kGroups; ++g) {
+        multiply((cur + g - 1) & 1, b, g, (b + NBUF - 1) % NBUF, g < kSpread ? kPer * g / kSpread : 0, g < kSpread ? kPer * (g + 1) / kSpread : 0);
+      }
       wait_loads<(NBUF - 2) * kPer>();
       __builtin_amdgcn_s_barrier();
-      half(1, s_buf + ((s + 1) % NBUF) * kStage, 0, s + NBUF);
+      clip(s + NBUF);
+      multiply((cur + kGroups - 1) & 1, (b + 1) % NBUF, 0, b, 0, kPer / kSpread);
+    };
+    // what the first stage's groups would request of the one before it has been requested
+#pragma unroll
+    for (int i = kPer / kSpread; i < kPer; ++i) src[i] -= kBK;
+    int s = 0;
+    for (; s + NBUF <= stages; s += NBUF) {
+#pragma unroll
+      for (int b = 0; b < NBUF; ++b) stage(s + b, b);
     }
+#pragma unroll
+    for (int b = 0; b < NBUF - 1; ++b)
+      if (s + b < stages) stage(s + b, b);
     wait_loads<0>();
   } else {
     i32x4 v[kPer];
@@ -365,7 +409,7 @@ hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
   else if (a.S <= 64) launch_few<1, 4, 8>(a, st);
   else if ((int64_t)((a.N + 255) / 256) * ((a.S + 255) / 256) >= 192) launch_tile<256, 256, 2, 2, 128, 2>(a, direct, st);
   else if ((int64_t)((a.N + 127) / 128) * ((a.S + 127) / 128) >= 192) launch_tile<128, 128, 2, 2, 128, 2>(a, direct, st);
-  else launch_tile<64, 64, 2, 2, 128, 3>(a, direct, st);
+  else launch_tile<64, 64, 2, 2, 128, 4>(a, direct, st);
   return hipGetLastError();
 }
 
