@@ -434,10 +434,15 @@ int moe_silu_quant(const void *g, const void *u, int32_t x_dtype, int64_t ldx, i
  *   y[s, n] = t(fp32(sum_k q[s, k] w[n, k]) * (d[s] * dw[n])),
  * the sum exact in int32 (K <= 131071).  q: [S, K] and d: [S] as written by the calls
  * above (any int8 values are taken); w: [N, K] two's complement bytes and dw: [N], the
- * interchange form of MOE_WF_Q8_ROW.  y: [S, N] of y_dtype.  ws: device workspace of at
- * least moe_qmatmul_workspace_bytes(S, N, K) bytes (that may be 0; ws may then be NULL),
- * 16-byte aligned, not initialised, used by one call at a time.  Also MOE_EWORKSPACE. */
-int64_t moe_qmatmul_workspace_bytes(int32_t S, int32_t N, int32_t K);
+ * interchange form of MOE_WF_Q8_ROW.  y: [S, N] of y_dtype.  Rows whose length and
+ * distance are multiples of 16 and that start at a multiple of 16 bytes are used where
+ * they lie.  Others may first be copied to such places, where that is faster: ws is a
+ * device workspace of at least moe_qmatmul_workspace_bytes bytes for the same operands (0
+ * where nothing is copied; ws may then be NULL), 16-byte aligned, not initialised, used
+ * by one call at a time.  A result does not depend on the other rows of the call.  Also
+ * MOE_EWORKSPACE. */
+int64_t moe_qmatmul_workspace_bytes(const int8_t *q, int64_t ldq, const int8_t *w, int64_t ldw, int32_t S, int32_t N,
+                                    int32_t K);
 int moe_qmatmul(const int8_t *q, int64_t ldq, const float *d, const int8_t *w, int64_t ldw, const float *dw, int32_t S,
                 int32_t N, int32_t K, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
 

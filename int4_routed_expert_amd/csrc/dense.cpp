@@ -69,27 +69,30 @@ int moe_silu_quant(const void *g, const void *u, int32_t x_dtype, int64_t ldx, i
   return status(launch_silu_quant(a, x_dtype == MOE_BF16, (hipStream_t)stream));
 }
 
-int64_t moe_qmatmul_workspace_bytes(int32_t S, int32_t N, int32_t K) {
-  if (S < 0 || N < 1 || K < 1 || K > 131071) return MOE_EINVAL;
-  return S == 0 ? 0 : qmatmul_workspace(S, N, K);
+int64_t moe_qmatmul_workspace_bytes(const int8_t *q, int64_t ldq, const int8_t *w, int64_t ldw, int32_t S, int32_t N,
+                                    int32_t K) {
+  if (S < 0 || N < 1 || K < 1 || K > 131071 || ldq < 0 || ldw < 0) return MOE_EINVAL;
+  if (S == 0) return 0;
+  QmmArgs a{};
+  a.S = S; a.N = N; a.K = K; a.q = q; a.w = w; a.ldq = ldq; a.ldw = ldw;
+  return qmatmul_workspace(a);
 }
 
 int moe_qmatmul(const int8_t *q, int64_t ldq, const float *d, const int8_t *w, int64_t ldw, const float *dw, int32_t S,
                 int32_t N, int32_t K, void *y, int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream) {
-  const int64_t need = moe_qmatmul_workspace_bytes(S, N, K);
+  const int64_t need = moe_qmatmul_workspace_bytes(q, ldq, w, ldw, S, N, K);
   if (need < 0) return (int)need;
   if (!known(y_dtype)) return MOE_EDTYPE;
   if (S == 0) return MOE_OK;
   if (!q || !d || !w || !dw || !y || (need > 0 && !ws)) return MOE_ENULL;
-  if (ldq < 0 || ldw < 0 || ldy < N || !aligned(d, 4) || !aligned(dw, 4) || !aligned(y, size_of(y_dtype)) ||
-      (need > 0 && !aligned(ws, 16)))
+  if (ldy < N || !aligned(d, 4) || !aligned(dw, 4) || !aligned(y, size_of(y_dtype)) || (need > 0 && !aligned(ws, 16)))
     return MOE_EINVAL;
   if ((uint64_t)need > ws_bytes) return MOE_EWORKSPACE;
   QmmArgs a{};
   a.S = S; a.N = N; a.K = K; a.y_bf16 = y_dtype == MOE_BF16;
   a.q = q; a.w = w; a.d = d; a.dw = dw; a.y = y;
   a.ldq = ldq; a.ldw = ldw; a.ldy = ldy;
-  a.part = need > 0 ? (int32_t *)ws : nullptr;
+  a.ws = (int8_t *)ws;
   return status(launch_qmatmul(a, (hipStream_t)stream));
 }
 

@@ -25,7 +25,7 @@ struct QmmArgs {
   const float *d, *dw;
   void *y;
   int64_t ldq, ldw, ldy;
-  int32_t *part;  // workspace
+  int8_t *ws;
 };
 
 struct RopeArgs {
@@ -64,7 +64,7 @@ __device__ inline void store_el(void *p, int64_t i, float v) {
 hipError_t launch_norm_quant(const RowArgs &a, int x_bf16, hipStream_t st);
 hipError_t launch_silu_quant(const RowArgs &a, int x_bf16, hipStream_t st);
 hipError_t launch_qmatmul(const QmmArgs &a, hipStream_t st);
-int64_t qmatmul_workspace(int S, int N, int K);
+int64_t qmatmul_workspace(const QmmArgs &a);
 hipError_t launch_rope(const RopeArgs &a, int x_bf16, int interleaved, hipStream_t st);
 
 }  // namespace moe

@@ -1,5 +1,8 @@
 // Product of int8 rows with int8 weights: y[s, n] = (sum_k q[s, k] w[n, k]) * (d[s] * dw[n]),
 // the sum exact in int32.
+#include <algorithm>
+#include <cmath>
+
 #include "dense.h"
 
 namespace moe {
@@ -7,13 +10,25 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef u32x4_t u32x4_any __attribute__((aligned(1)));
+typedef u32x4_t u32x4_w __attribute__((aligned(4)));
 
 __device__ const uint8_t g_zeros[16] __attribute__((aligned(16))) = {};
 
-// 16 bytes at any address.
+// 16 bytes at p.  W4: p lies on a whole word; else the words that hold them (every one
+// holds at least one of them) are read and shifted together: a load from an odd address
+// takes the hardware several times as long (one token, 4096 x 6143: 13.8 us against 7.1).
+template <bool W4>
 __device__ inline i32x4 load16(const int8_t *p) {
-  return __builtin_bit_cast(i32x4, *(const __attribute__((address_space(1))) u32x4_any *)p);
+  if constexpr (W4) {
+    return __builtin_bit_cast(i32x4, *(const __attribute__((address_space(1))) u32x4_w *)p);
+  } else {
+    const int8_t *base = (const int8_t *)((uintptr_t)p & ~(uintptr_t)3);
+    const u32x4_t d = *(const __attribute__((address_space(1))) u32x4_w *)base;
+    const uint32_t e = ldg<uint32_t>((const int8_t *)((uintptr_t)(p + 15) & ~(uintptr_t)3));
+    const uint32_t sh = (uint32_t)(uintptr_t)p & 3;
+    return i32x4{(int)__builtin_amdgcn_alignbyte(d.y, d.x, sh), (int)__builtin_amdgcn_alignbyte(d.z, d.y, sh),
+                 (int)__builtin_amdgcn_alignbyte(d.w, d.z, sh), (int)__builtin_amdgcn_alignbyte(e, d.w, sh)};
+  }
 }
 
 // Bytes [k, k + 16) of a row of K bytes, zeros beyond its end.  The row's last, partial
@@ -21,10 +36,10 @@ __device__ inline i32x4 load16(const int8_t *p) {
 // row is touched.
 __device__ inline i32x4 load16_tail(const int8_t *row, int k, int K) {
   i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) return load16(row + k);
   if (k >= K) return v;
+  if (k + 16 <= K) return load16<false>(row + k);
   if (K >= 16) {
-    const u32x4_t r = __builtin_bit_cast(u32x4_t, load16(row + K - 16));
+    const u32x4_t r = __builtin_bit_cast(u32x4_t, load16<false>(row + K - 16));
     const int drop = k + 16 - K;  // 1..15 bytes of the previous chunk in front
     unsigned __int128 x = ((unsigned __int128)(((uint64_t)r.w << 32) | r.z) << 64) | (((uint64_t)r.y << 32) | r.x);
     x >>= 8 * drop;
@@ -56,17 +71,114 @@ __device__ inline void store4(const QmmArgs &a, int64_t s, int n, float v0, floa
   }
 }
 
+// ---- up to eight tokens -----------------------------------------------------------
+// Bound by the weights, each read once.  A wave takes R weight rows and meets them and
+// the NS tokens in runs of 1 KB, 16 bytes a lane (whole rows of cache lines: 16 rows of 64
+// bytes a load, as the matrix instruction wants them, reach half the rate), multiplies
+// with v_dot4 and adds up over its lanes.  KS waves share a row where rows are few.
+__device__ inline int dot16(i32x4 a, i32x4 b, int c) {
+  c = __builtin_amdgcn_sdot4(a[0], b[0], c, false);
+  c = __builtin_amdgcn_sdot4(a[1], b[1], c, false);
+  c = __builtin_amdgcn_sdot4(a[2], b[2], c, false);
+  return __builtin_amdgcn_sdot4(a[3], b[3], c, false);
+}
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ inline int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
+}
+__device__ inline int wave_total(int v) {  // the sum over the lanes, in every lane
+  v = dpp_add<0xB1>(v);        // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E>(v);        // quad_perm [2,3,0,1]
+  v = dpp_add<0x141>(v);       // row_half_mirror
+  v = dpp_add<0x140>(v);       // row_mirror
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast:31
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+template <int NS, int R, int KS, bool W4>
+__global__ __launch_bounds__(256) void k_qmm_vec(QmmArgs a) {
+  constexpr int kU = R + NS <= 2 ? 6 : R + NS <= 5 ? 4 : 2;  // runs in flight
+  static_assert(R * NS <= 64, "an output a lane");
+  __shared__ int s_sum[4][R * NS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int part = wave % KS;
+  const int64_t n0 = ((int64_t)blockIdx.x * (4 / KS) + wave / KS) * R;
+  const int8_t *wr[R], *qr[NS];
+#pragma unroll
+  for (int r = 0; r < R; ++r) wr[r] = a.w + min(n0 + r, (int64_t)a.N - 1) * a.ldw;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) qr[s] = a.q + (int64_t)min(s, a.S - 1) * a.ldq;
+  int acc[R][NS] = {};
+  const int whole = a.K & ~15;
+  int k = (part * 64 + lane) * 16;
+  auto meet = [&](auto load) __attribute__((always_inline)) {
+    i32x4 W[R], Q[NS];
+#pragma unroll
+    for (int r = 0; r < R; ++r) W[r] = load(wr[r]);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) Q[s] = load(qr[s]);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) acc[r][s] = dot16(W[r], Q[s], acc[r][s]);
+  };
+  for (; k + (kU - 1) * KS * 1024 < whole; k += kU * KS * 1024) {
+    i32x4 W[kU][R], Q[kU][NS];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) W[u][r] = load16<W4>(wr[r] + k + u * KS * 1024);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) Q[u][s] = load16<W4>(qr[s] + k + u * KS * 1024);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) acc[r][s] = dot16(W[u][r], Q[u][s], acc[r][s]);
+  }
+  for (; k < whole; k += KS * 1024) meet([&](const int8_t *row) { return load16<W4>(row + k); });
+  if (k < a.K) meet([&](const int8_t *row) { return load16_tail(row, k, a.K); });
+  int mine = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int t = wave_total(acc[r][s]);
+      mine = lane == s * R + r ? t : mine;
+    }
+  if constexpr (KS > 1) {
+    if (lane < R * NS) s_sum[wave][lane] = mine;
+    __syncthreads();
+    if (part) return;
+    if (lane < R * NS) {
+#pragma unroll
+      for (int i = 1; i < KS; ++i) mine += s_sum[wave + i][lane];
+    }
+  }
+  const int s = lane / R;
+  const int64_t n = n0 + lane % R;
+  if (lane < R * NS && s < a.S && n < a.N) {
+    const float v = (float)mine * (ldg<float>(a.d + s) * ldg<float>(a.dw + n));
+    if (a.y_bf16) store_el<true>(a.y, s * a.ldy + n, v);
+    else store_el<false>(a.y, s * a.ldy + n, v);
+  }
+}
+
 // ---- few tokens ------------------------------------------------------------------
 // A workgroup takes 16 MT weight rows and all the tokens (NT blocks of 16); its waves
 // split K and add their int32 sums in LDS.  v_mfma_i32_16x16x64_i8 with the weights as
 // rows and the tokens as columns, both operands straight from memory: lane l holds 16
 // bytes of row (or token) l % 16 at k + 16 (l / 16).
-template <int MT, int NT, int W>
+template <int MT, int NT, int W, bool W4>
 __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
   constexpr int kU = MT * NT >= 4 ? 2 : 4;  // k steps in flight
   __shared__ i32x4 s_acc[W][MT * NT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16 * MT, s0 = blockIdx.y * 16 * NT;
+  const int nb = (a.N + 16 * MT - 1) / (16 * MT);
+  const int n0 = (int)(blockIdx.x % nb) * 16 * MT, s0 = (int)(blockIdx.x / nb) * 16 * NT;
   const int col = lane & 15, kq = (lane >> 4) * 16;
   const int8_t *wr[MT], *qr[NT];
 #pragma unroll
@@ -83,9 +195,9 @@ __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) A[u][m] = load16(wr[m] + (st + u) * 64);
+      for (int m = 0; m < MT; ++m) A[u][m] = load16<W4>(wr[m] + (st + u) * 64);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) B[u][t] = load16(qr[t] + (st + u) * 64);
+      for (int t = 0; t < NT; ++t) B[u][t] = load16<W4>(qr[t] + (st + u) * 64);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u)
@@ -98,9 +210,9 @@ __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
   for (; st < hi; ++st) {
     i32x4 A[MT], B[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) A[m] = load16(wr[m] + st * 64);
+    for (int m = 0; m < MT; ++m) A[m] = load16<W4>(wr[m] + st * 64);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) B[t] = load16(qr[t] + st * 64);
+    for (int t = 0; t < NT; ++t) B[t] = load16<W4>(qr[t] + st * 64);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -169,7 +281,7 @@ __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int BN, int BS, int WN, int WS, int kBK, int NBUF, bool DIRECT>
+template <int BN, int BS, int WN, int WS, int kBK, int NBUF>
 __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
   constexpr int kThr = 64 * WN * WS;
   constexpr int TN = BN / WN / 32, TS = BS / WS / 32;  // 32x32 blocks of a wave
@@ -231,121 +343,86 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
     return *(const i32x4 *)(buf + (f < TN ? at_w[kk] + f * 32 * kBK : at_t[kk] + (f - TN) * 32 * kBK));
   };
 
-  if constexpr (DIRECT) {
-    // The wait for a stage leaves the requests of the stages after it in flight, so the
-    // requests are written in assembly: a load into LDS known to the compiler makes it
-    // wait for all of them before the next read of LDS.  A wave issues one instruction in
-    // about four cycles, so what surrounds the MFMAs is kept short: the sources advance by
-    // a stage, and only near the end of K are chunks beyond it pointed at zeros.
-    constexpr int kF = TN + TS, kM = TN * TS;
-    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
-        (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024);
+  // The wait for a stage leaves the requests of the stages after it in flight, so the
+  // requests are written in assembly: a load into LDS known to the compiler makes it
+  // wait for all of them before the next read of LDS.  A wave issues one instruction in
+  // about four cycles, so what surrounds the MFMAs is kept short: the sources advance by
+  // a stage, and only near the end of K are chunks beyond it pointed at zeros.
+  constexpr int kF = TN + TS, kM = TN * TS;
+  const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
+      (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) src[i] += kc[i];
-    auto clip = [&](int s) __attribute__((always_inline)) {  // before stage s is requested
-      if (s >= whole) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if ((int64_t)s * kBK + kc[i] >= a.K) src[i] = (const int8_t *)g_zeros;
-      }
-    };
-    auto request = [&](int i, int buffer) __attribute__((always_inline)) {
-      load_to_lds(src[i], lds, buffer * kStage + i * kThr * 16);
-      src[i] += kBK;
-    };
-#pragma unroll
-    for (int s = 0; s < NBUF; ++s) {
-      clip(s);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) request(i, s);
-    }
-    wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
-    // Fragments are read a group of kG k steps ahead, at least 4 MFMAs: they take longer to
-    // arrive than one MFMA takes.
-    constexpr int kG = kM >= 4 ? (kM >= 8 ? 1 : 2) : kSteps < 4 ? kSteps : 4, kGroups = kSteps / kG;
-    static_assert(kSteps % kG == 0 && NBUF % 2 == 0, "groups of k steps");
-    i32x4 F[2][kG][kF];
-#pragma unroll
-    for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
-    // Multiply one group's fragments while the next group's are read and, in a stage's last
-    // group, the stage just read is requested anew, spread between the MFMAs.
-    auto multiply = [&](int cur, int buffer, int g, int again, int r0, int r1) __attribute__((always_inline)) {
-      constexpr int kAll = kG * kM;
-#pragma unroll
-      for (int m = 0; m < kAll; ++m) {
-#pragma unroll
-        for (int f = 0; f < kG * kF; ++f)
-          if (f * kAll / (kG * kF) == m) F[cur ^ 1][f / kF][f % kF] = frag(s_buf + buffer * kStage, f % kF, g * kG + f / kF);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
-        const int k = m / kM, i = m % kM / TS, j = m % TS;
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F[cur][k][i], F[cur][k][TN + j], acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    // A stage's new requests go out over its own last group and the first of the next stage:
-    // all in one group they wait for each other (8192x12288x6144: 582 us, 558 over two, 571
-    // over four, where the last arrive late).
-    constexpr int kSpread = kGroups > 1 ? 2 : 1;
-    auto stage = [&](int s, int b) __attribute__((always_inline)) {  // stage s, in buffer b
-      const int cur = b * kGroups & 1;
-#pragma unroll
-      for (int g = 1; g < kGroups; ++g) {
-        multiply((cur + g - 1) & 1, b, g, (b + NBUF - 1) % NBUF, g < kSpread ? kPer * g / kSpread : 0, g < kSpread ? kPer * (g + 1) / kSpread : 0);
-      }
-      wait_loads<(NBUF - 2) * kPer>();
-      __builtin_amdgcn_s_barrier();
-      clip(s + NBUF);
-      multiply((cur + kGroups - 1) & 1, (b + 1) % NBUF, 0, b, 0, kPer / kSpread);
-    };
-    // what the first stage's groups would request of the one before it has been requested
-#pragma unroll
-    for (int i = kPer / kSpread; i < kPer; ++i) src[i] -= kBK;
-    int s = 0;
-    for (; s + NBUF <= stages; s += NBUF) {
-#pragma unroll
-      for (int b = 0; b < NBUF; ++b) stage(s + b, b);
-    }
-#pragma unroll
-    for (int b = 0; b < NBUF - 1; ++b)
-      if (s + b < stages) stage(s + b, b);
-    wait_loads<0>();
-  } else {
-    i32x4 v[kPer];
-    auto fetch = [&](int s) {
+  for (int i = 0; i < kPer; ++i) src[i] += kc[i];
+  auto clip = [&](int s) __attribute__((always_inline)) {  // before stage s is requested
+    if (s >= whole) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        v[i] = s < whole ? load16(src[i] + (int64_t)s * kBK + kc[i]) : load16_tail(src[i], s * kBK + kc[i], a.K);
-    };
-    auto put = [&](int s) {
-      uint8_t *base = s_buf + (s % NBUF) * kStage;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) *(i32x4 *)(base + (threadIdx.x + i * kThr) * 16) = v[i];
-    };
-    fetch(0);
-    put(0);
-    for (int s = 0; s < stages; ++s) {
-      if (s + 1 < stages) fetch(s + 1);
-      __syncthreads();
-      const uint8_t *buf = s_buf + (s % NBUF) * kStage;
-#pragma unroll
-      for (int kk = 0; kk < kBK / 32; ++kk) {
-        i32x4 A[TN], B[TS];
-#pragma unroll
-        for (int i = 0; i < TN; ++i) A[i] = frag(buf, i, kk);
-#pragma unroll
-        for (int j = 0; j < TS; ++j) B[j] = frag(buf, TN + j, kk);
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-          for (int j = 0; j < TS; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(A[i], B[j], acc[i][j], 0, 0, 0);
-      }
-      if (s + 1 < stages) put(s + 1);
+        if ((int64_t)s * kBK + kc[i] >= a.K) src[i] = (const int8_t *)g_zeros;
     }
+  };
+  auto request = [&](int i, int buffer) __attribute__((always_inline)) {
+    load_to_lds(src[i], lds, buffer * kStage + i * kThr * 16);
+    src[i] += kBK;
+  };
+#pragma unroll
+  for (int s = 0; s < NBUF; ++s) {
+    clip(s);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) request(i, s);
   }
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  // Fragments are read a group of kG k steps ahead, at least 4 MFMAs: they take longer to
+  // arrive than one MFMA takes.
+  constexpr int kG = kM >= 4 ? (kM >= 8 ? 1 : 2) : kSteps < 4 ? kSteps : 4, kGroups = kSteps / kG;
+  static_assert(kSteps % kG == 0 && NBUF % 2 == 0, "groups of k steps");
+  i32x4 F[2][kG][kF];
+#pragma unroll
+  for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
+  // Multiply one group's fragments while the next group's are read and, in a stage's last
+  // group, the stage just read is requested anew, spread between the MFMAs.
+  auto multiply = [&](int cur, int buffer, int g, int again, int r0, int r1) __attribute__((always_inline)) {
+    constexpr int kAll = kG * kM;
+#pragma unroll
+    for (int m = 0; m < kAll; ++m) {
+#pragma unroll
+      for (int f = 0; f < kG * kF; ++f)
+        if (f * kAll / (kG * kF) == m) F[cur ^ 1][f / kF][f % kF] = frag(s_buf + buffer * kStage, f % kF, g * kG + f / kF);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
+      const int k = m / kM, i = m % kM / TS, j = m % TS;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F[cur][k][i], F[cur][k][TN + j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // A stage's new requests go out over its own last group and the first of the next stage:
+  // all in one group they wait for each other (8192x12288x6144: 582 us, 558 over two, 571
+  // over four, where the last arrive late).
+  constexpr int kSpread = kGroups > 1 ? 2 : 1;
+  auto stage = [&](int s, int b) __attribute__((always_inline)) {  // stage s, in buffer b
+    const int cur = b * kGroups & 1;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      multiply((cur + g - 1) & 1, b, g, (b + NBUF - 1) % NBUF, g < kSpread ? kPer * g / kSpread : 0, g < kSpread ? kPer * (g + 1) / kSpread : 0);
+    }
+    wait_loads<(NBUF - 2) * kPer>();
+    __builtin_amdgcn_s_barrier();
+    clip(s + NBUF);
+    multiply((cur + kGroups - 1) & 1, (b + 1) % NBUF, 0, b, 0, kPer / kSpread);
+  };
+  // what the first stage's groups would request of the one before it has been requested
+#pragma unroll
+  for (int i = kPer / kSpread; i < kPer; ++i) src[i] -= kBK;
+  int s = 0;
+  for (; s + NBUF <= stages; s += NBUF) {
+#pragma unroll
+    for (int b = 0; b < NBUF; ++b) stage(s + b, b);
+  }
+#pragma unroll
+  for (int b = 0; b < NBUF - 1; ++b)
+    if (s + b < stages) stage(s + b, b);
+  wait_loads<0>();
 
   // Each wave turns its sums round in its own part of the buffers, 32 tokens at a time, so
   // that they leave as runs of a token's neighbouring outputs.
@@ -379,38 +456,178 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   }
 }
 
-template <int MT, int NT, int W>
+// ---- rows on 16-byte boundaries ------------------------------------------------------
+// Copies the token rows, the weight rows or both to the workspace, each at a multiple of
+// 16 bytes and with zeros up to one: the loads into LDS need that.  One wave a row.
+__global__ __launch_bounds__(256) void k_qmm_align(QmmArgs a, int8_t *q, int8_t *w, int ld) {
+  const int64_t rows_q = q ? a.S : 0, rows = rows_q + (w ? a.N : 0);
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
+    const int8_t *from = r < rows_q ? a.q + r * a.ldq : a.w + (r - rows_q) * a.ldw;
+    int8_t *to = r < rows_q ? q + r * ld : w + (r - rows_q) * ld;
+#pragma unroll 2
+    for (int k = (threadIdx.x & 63) * 16; k < ld; k += 1024) {
+      const i32x4 v = load16_tail(from, k, a.K);
+      stg<uint4>(to + k, make_uint4((uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]));
+    }
+  }
+}
+
+// ---- which kernel --------------------------------------------------------------------
+enum QmmKernel { kVec, kFew1, kFew2, kTile32x64, kTile64, kTile64x128, kTile128, kTile128Two, kTile256 };
+
+bool on16(const int8_t *p, int64_t ld, int rows, int K) {
+  return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && K % 16 == 0;
+}
+
+struct QmmPlan {
+  QmmKernel kernel;
+  bool copy_q, copy_w;  // rows that the tiles need on 16-byte boundaries first
+  int64_t bytes_q, bytes;  // workspace: of the token rows, of all
+};
+
+// The kernel with the least estimated time, from times measured on whole chips (us): a
+// tile kernel's rounds of workgroups over its slots, each round a part for its start and
+// end and a part for every 128 of K.  The direct kernel moves 39 KB/us for a workgroup.
+QmmPlan plan_of(const QmmArgs &a) {
+  QmmPlan p{};
+  const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);
+  if (a.S <= 4) {
+    p.kernel = kVec;
+    return p;
+  }
+  struct Tile { QmmKernel kernel; int n, s, slots; double once, stage; };
+  static constexpr Tile kTiles[] = {
+      {kTile32x64, 32, 64, 256, 2.8, 0.17},   {kTile64, 64, 64, 256, 2.8, 0.205}, {kTile64x128, 64, 128, 256, 3.0, 0.34},
+      {kTile128, 128, 128, 256, 2.2, 0.60},   {kTile128Two, 128, 128, 512, 2.5, 1.1},
+      {kTile256, 256, 256, 256, 21.0, 1.47}};
+  const double stages = (a.K + 127) / 128;
+  const int64_t ld = ((int64_t)a.K + 15) / 16 * 16;
+  const double moved = 2.0 * ((q16 ? 0 : a.S * ld) + (w16 ? 0 : a.N * ld));
+  const double copy = moved > 0 ? 3.0 + moved / 4e6 : 0.0;
+  double best = 1e30;
+  for (int nt = 1; nt <= 2; ++nt) {
+    const double groups = (double)((a.N + 15) / 16) * ((a.S + 16 * nt - 1) / (16 * nt));
+    const double t = 2.7 + std::max(1.0, groups / 256) * 16 * (1 + nt) * a.K / 39e3;
+    if (t < best && groups <= 1 << 18) {
+      best = t;
+      p.kernel = nt == 1 ? kFew1 : kFew2;
+    }
+  }
+  for (const Tile &t : kTiles) {
+    const double tiles = (double)((a.N + t.n - 1) / t.n) * ((a.S + t.s - 1) / t.s);
+    const double us = copy + std::ceil(tiles / t.slots) * (t.once + t.stage * stages);
+    if (us < best) {
+      best = us;
+      p.kernel = t.kernel;
+    }
+  }
+  if (p.kernel >= kTile32x64) {
+    p.copy_q = !q16;
+    p.copy_w = !w16;
+    p.bytes_q = q16 ? 0 : a.S * ld;
+    p.bytes = p.bytes_q + (w16 ? 0 : a.N * ld);
+  }
+  return p;
+}
+
+template <int NS, int R, int KS, bool W4>
+void launch_vec(const QmmArgs &a, hipStream_t st) {
+  const int rows = R * 4 / KS;
+  MOE_LAUNCH((k_qmm_vec<NS, R, KS, W4>), dim3((unsigned)((a.N + rows - 1) / rows)), dim3(256), 0, st, a);
+}
+
+template <int NS, bool W4>
+void launch_vec_for(const QmmArgs &a, hipStream_t st) {
+  // few rows: four waves share one; more: two rows a wave meet the same tokens
+  if (a.N <= 1024) launch_vec<NS, 1, 4, W4>(a, st);
+  else if (a.N <= 8192) launch_vec<NS, 1, 1, W4>(a, st);
+  else launch_vec<NS, 2, 1, W4>(a, st);
+}
+
+template <int NT, bool W4>
 void launch_few(const QmmArgs &a, hipStream_t st) {
-  const dim3 g((unsigned)((a.N + 16 * MT - 1) / (16 * MT)), (unsigned)((a.S + 16 * NT - 1) / (16 * NT)));
-  MOE_LAUNCH((k_qmm_few<MT, NT, W>), g, dim3(64 * W), 0, st, a);
+  const unsigned groups = (unsigned)((a.N + 15) / 16) * (unsigned)((a.S + 16 * NT - 1) / (16 * NT));
+  MOE_LAUNCH((k_qmm_few<1, NT, 8, W4>), dim3(groups), dim3(512), 0, st, a);
+}
+
+template <bool W4>
+void launch_direct(const QmmArgs &a, QmmKernel k, hipStream_t st) {
+  if (k == kFew1) launch_few<1, W4>(a, st);
+  else if (k == kFew2) launch_few<2, W4>(a, st);
+  else if (a.S == 1) launch_vec_for<1, W4>(a, st);
+  else if (a.S == 2) launch_vec_for<2, W4>(a, st);
+  else launch_vec_for<4, W4>(a, st);
 }
 
 template <int BN, int BS, int WN, int WS, int BK, int NBUF>
-void launch_tile(const QmmArgs &a, bool direct, hipStream_t st) {
+void launch_tile(const QmmArgs &a, hipStream_t st) {
   const int tn = (a.N + BN - 1) / BN, ts = (a.S + BS - 1) / BS;
   const int64_t total = (int64_t)tn * ts;
   const dim3 g((unsigned)((total + kXcds - 1) / kXcds * kXcds));
   const int group = 4;
-  if (direct) MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, BK, NBUF, true>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
-  else MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, 64, 2, false>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
+  MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, BK, NBUF>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
 }
 
 }  // namespace
 
-int64_t qmatmul_workspace(int, int, int) { return 0; }
+int64_t qmatmul_workspace(const QmmArgs &a) { return plan_of(a).bytes; }
+
+namespace {
+
+void launch_piece(const QmmArgs &a, QmmKernel kernel, hipStream_t st) {
+  switch (kernel) {
+    case kVec: case kFew1: case kFew2: {
+      const bool w4 = (uintptr_t)a.q % 4 == 0 && (uintptr_t)a.w % 4 == 0 && (a.S == 1 || a.ldq % 4 == 0) &&
+                      (a.N == 1 || a.ldw % 4 == 0);
+      if (w4) launch_direct<true>(a, kernel, st);
+      else launch_direct<false>(a, kernel, st);
+      break;
+    }
+    case kTile32x64: launch_tile<32, 64, 1, 2, 128, 4>(a, st); break;
+    case kTile64: launch_tile<64, 64, 2, 2, 128, 4>(a, st); break;
+    case kTile64x128: launch_tile<64, 128, 2, 4, 128, 4>(a, st); break;
+    case kTile128: launch_tile<128, 128, 2, 4, 128, 4>(a, st); break;
+    case kTile128Two: launch_tile<128, 128, 2, 2, 128, 2>(a, st); break;
+    case kTile256: launch_tile<256, 256, 2, 2, 128, 2>(a, st); break;
+  }
+}
+
+}  // namespace
 
 hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
-  ProfScope ps("qmatmul", st);
   QmmArgs a = a0;
   a.y_vec = (uintptr_t)a.y % (a.y_bf16 ? 8 : 16) == 0 && a.ldy % 4 == 0;
-  const bool direct = (uintptr_t)a.q % 16 == 0 && (uintptr_t)a.w % 16 == 0 && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.K % 16 == 0;
-  if (a.S <= 16) launch_few<1, 1, 8>(a, st);
-  else if (a.S <= 32) launch_few<1, 2, 8>(a, st);
-  else if (a.S <= 64) launch_few<1, 4, 8>(a, st);
-  else if ((int64_t)((a.N + 255) / 256) * ((a.S + 255) / 256) >= 192) launch_tile<256, 256, 2, 2, 128, 2>(a, direct, st);
-  else if ((int64_t)((a.N + 127) / 128) * ((a.S + 127) / 128) >= 192) launch_tile<128, 128, 2, 2, 128, 2>(a, direct, st);
-  else launch_tile<64, 64, 2, 2, 128, 4>(a, direct, st);
-  return hipGetLastError();
+  const QmmPlan p = plan_of(a);
+  if (p.copy_q || p.copy_w) {
+    ProfScope ps("qmatmul_align", st);
+    int8_t *q = p.copy_q ? a.ws : nullptr, *w = p.copy_w ? a.ws + p.bytes_q : nullptr;
+    const int ld = (a.K + 15) / 16 * 16;
+    const int64_t rows = (q ? (int64_t)a.S : 0) + (w ? (int64_t)a.N : 0);
+    MOE_LAUNCH(k_qmm_align, dim3((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 18)), dim3(256), 0, st, a, q, w, ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (q) a.q = q, a.ldq = ld;
+    if (w) a.w = w, a.ldw = ld;
+    a.K = ld;
+  }
+  // a launch holds fewer than 2^32 threads: very long operands go in pieces
+  constexpr int kMost = 1 << 18;
+  for (int64_t s = 0; s < a.S; s += kMost)
+    for (int64_t n = 0; n < a.N; n += kMost) {
+      QmmArgs c = a;
+      c.S = (int)std::min<int64_t>(kMost, a.S - s);
+      c.N = (int)std::min<int64_t>(kMost, a.N - n);
+      c.q += s * a.ldq;
+      c.w += n * a.ldw;
+      c.d += s;
+      c.dw += n;
+      c.y = (char *)a.y + (s * a.ldy + n) * (a.y_bf16 ? 2 : 4);
+      ProfScope ps(p.kernel <= kFew2 ? "qmatmul_direct" : "qmatmul_tile", st);
+      launch_piece(c, p.kernel, st);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
 }
 
 }  // namespace moe

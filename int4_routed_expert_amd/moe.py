@@ -104,7 +104,7 @@ def _load():
         "moe_pool_check_view": (ctypes.c_int, [p, i32, ctypes.POINTER(moe_slot_view)]),
         "moe_norm_quant": (ctypes.c_int, [p, i32, i64, p, i64, p, i32, f32, i32, i32, p, i64, p, i32, i64, p, i64, p, p]),
         "moe_silu_quant": (ctypes.c_int, [p, p, i32, i64, i32, i32, p, i32, i64, p, i64, p, p]),
-        "moe_qmatmul_workspace_bytes": (i64, [i32, i32, i32]),
+        "moe_qmatmul_workspace_bytes": (i64, [p, i64, p, i64, i32, i32, i32]),
         "moe_qmatmul": (ctypes.c_int, [p, i64, p, p, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
         "moe_rope": (ctypes.c_int, [rp, rp, i32, i32, i32, i32, i32, i32, p, i32, p, f32, p]),
         "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f32)]),
@@ -344,8 +344,8 @@ def moe_silu_quant(g, u, x_dtype: int, ldx: int, S: int, I: int, y, y_dtype: int
                                stream_handle(stream)), "moe_silu_quant")
 
 
-def moe_qmatmul_workspace_bytes(S: int, N: int, K: int) -> int:
-    return _lib.moe_qmatmul_workspace_bytes(S, N, K)
+def moe_qmatmul_workspace_bytes(q, ldq: int, w, ldw: int, S: int, N: int, K: int) -> int:
+    return _lib.moe_qmatmul_workspace_bytes(ptr(q), ldq, ptr(w), ldw, S, N, K)
 
 
 def moe_qmatmul(q, ldq: int, d, w, ldw: int, dw, S: int, N: int, K: int, y, y_dtype: int, ldy: int, ws, ws_bytes: int,
@@ -529,12 +529,15 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
     gpu = _gpu(q, d, w, dw, ws)
     if stream is not None or gpu != torch.cuda.current_device():
         return _elsewhere(gpu, stream, qmatmul, (q, d, w, dw, ws), q, d, w, dw, out_dtype, ws)
-    need = _lib.moe_qmatmul_workspace_bytes(S, N, K)
-    if need > 0 and ws is None:
-        ws = q.new_empty(need)
+    pq, pw = q.data_ptr(), w.data_ptr()
+    # operands on 16-byte boundaries take no workspace
+    if ws is None and (pq | pw | ldq | ldw | K) & 15:
+        need = _lib.moe_qmatmul_workspace_bytes(pq, ldq, pw, ldw, S, N, K)
+        if need > 0:
+            ws = q.new_empty(need)
+    pws, nws = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     y = d.new_empty((S, N), dtype=out_dtype)
-    rc = _lib.moe_qmatmul(q.data_ptr(), ldq, d.data_ptr(), w.data_ptr(), ldw, dw.data_ptr(), S, N, K, y.data_ptr(), yd, N,
-                          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+    rc = _lib.moe_qmatmul(pq, ldq, d.data_ptr(), pw, ldw, dw.data_ptr(), S, N, K, y.data_ptr(), yd, N, pws, nws,
                           _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_qmatmul")

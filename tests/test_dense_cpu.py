@@ -58,18 +58,27 @@ def test_product_refusals(bad, status):
 
 
 def test_product_workspace():
-    """The size is never negative for sizes in range, and a workspace is required exactly where it is not 0."""
-    for S, N, K in [(1, 1, 1), (1, 4096, 6144), (16, 576, 16384), (64, 576, 16384), (256, 6144, 6144), (8192, 12288, 6144),
-                    (77, 577, 1111), (1, 1, 131071)]:
-        need = M.moe_qmatmul_workspace_bytes(S, N, K)
-        assert 0 <= need <= 1 << 30
-        if need:
-            assert product(S=S, N=N, K=K, ldy=N, ws=None) == M.MOE_ENULL
-            assert product(S=S, N=N, K=K, ldy=N, ws=A + 4) == M.MOE_EINVAL
-            assert product(S=S, N=N, K=K, ldy=N, wb=need - 1) == M.MOE_EWORKSPACE
-    assert M.moe_qmatmul_workspace_bytes(0, 64, 64) == 0
+    """Operands on 16-byte boundaries need none; for others the size is the copies' and a workspace is required exactly
+    where it is not 0."""
+    sizes = [(1, 1, 1), (1, 4096, 6144), (16, 576, 16384), (64, 576, 16384), (256, 6144, 6144), (8192, 12288, 6144),
+             (77, 577, 1111), (600, 4097, 6143), (1, 1, 131071), (500, 300, 131071)]
+    seen = 0
+    for S, N, K in sizes:
+        for off, ld in ((0, K), (0, K + 5), (1, K + 16)):
+            args = dict(q=A + off, ldq=ld, w=A + off, ldw=ld, S=S, N=N, K=K)
+            need = M.moe_qmatmul_workspace_bytes(args["q"], ld, args["w"], ld, S, N, K)
+            assert 0 <= need <= (S + N) * (K + 15)
+            if off == 0 and ld % 16 == 0 and K % 16 == 0:
+                assert need == 0
+            if need:
+                seen += 1
+                assert product(**args, ldy=N, ws=None) == M.MOE_ENULL
+                assert product(**args, ldy=N, ws=A + 4) == M.MOE_EINVAL
+                assert product(**args, ldy=N, wb=need - 1) == M.MOE_EWORKSPACE
+    assert seen
+    assert M.moe_qmatmul_workspace_bytes(None, 64, None, 64, 0, 64, 64) == 0
     for S, N, K in [(-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 131072)]:
-        assert M.moe_qmatmul_workspace_bytes(S, N, K) == M.MOE_EINVAL
+        assert M.moe_qmatmul_workspace_bytes(A, 64, A, 64, S, N, K) == M.MOE_EINVAL
 
 
 def turn(q=(A, A, 256, 64, 256, 64, 4), k=(A, A, 64, 64, 64, 64, 1), xd=0, S=2, D=64, rot=64, offset=0, layout=0, pos=A,

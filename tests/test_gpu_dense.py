@@ -294,7 +294,7 @@ def test_product_into_wider_rows(M):
         q, d, w, dw = operands(g, S, N, K)
         for dtype in (F32, BF):
             y = torch.full((S, N + 9), 5.0, dtype=dtype, device="cuda")
-            ws = torch.empty(max(16, M.moe_qmatmul_workspace_bytes(S, N, K)), dtype=torch.uint8, device="cuda")
+            ws = torch.empty(max(16, M.moe_qmatmul_workspace_bytes(q, K, w, K, S, N, K)), dtype=torch.uint8, device="cuda")
             M.moe_qmatmul(q, K, d, w, K, dw, S, N, K, y, M._code(dtype, "y"), N + 9, ws, ws.numel())
             assert torch.equal(y[:, :N].cpu(), product64(q, d, w, dw, dtype)) and (y[:, N:] == 5).all()
 
@@ -401,7 +401,7 @@ def test_offsets_beyond_32_bits(M):
     wf.copy_(w[:3])
     assert torch.equal(M.qmatmul(q, d, wf, dw[:3], out_dtype=F32), M.qmatmul(q, d, w[:3].contiguous(), dw[:3], out_dtype=F32))
     yf = buf.view(BF).as_strided((3, 40), (far // 2, 1), 1024)  # 2^31 elements and their bytes beyond 2^32
-    ws = torch.empty(max(16, M.moe_qmatmul_workspace_bytes(3, 40, 512)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(16, M.moe_qmatmul_workspace_bytes(q, 512, w, 512, 3, 40, 512)), dtype=torch.uint8, device="cuda")
     M.moe_qmatmul(q, 512, d, w, 512, dw, 3, 40, 512, yf, M.MOE_BF16, far // 2, ws, ws.numel())
     assert torch.equal(yf, M.qmatmul(q, d, w, dw))
     x = rows(g, 3, 1024, BF)
