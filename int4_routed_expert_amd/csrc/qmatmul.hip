@@ -485,9 +485,10 @@ struct QmmPlan {
   int64_t bytes_q, bytes;  // workspace: of the token rows, of all
 };
 
-// The kernel with the least estimated time, from times measured on whole chips (us): a
-// tile kernel's rounds of workgroups over its slots, each round a part for its start and
-// end and a part for every 128 of K.  The direct kernel moves 39 KB/us for a workgroup.
+// The kernel with the least estimated time, from times measured over 50 shapes (us).  A
+// tile kernel: 1.5, and for each round of 256 tiles (one a compute unit) a part for its
+// start and end and a part for every 128 of K (both with `together` tiles on a unit), or the time in which one tile alone gets
+// through K.  The direct kernel: 2.7, and each workgroup moves 39 KB/us.
 QmmPlan plan_of(const QmmArgs &a) {
   QmmPlan p{};
   const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);
@@ -495,11 +496,11 @@ QmmPlan plan_of(const QmmArgs &a) {
     p.kernel = kVec;
     return p;
   }
-  struct Tile { QmmKernel kernel; int n, s, slots; double once, stage; };
+  struct Tile { QmmKernel kernel; int n, s, together; double once, stage, alone; };
   static constexpr Tile kTiles[] = {
-      {kTile32x64, 32, 64, 256, 2.8, 0.17},   {kTile64, 64, 64, 256, 2.8, 0.205}, {kTile64x128, 64, 128, 256, 3.0, 0.34},
-      {kTile128, 128, 128, 256, 2.2, 0.60},   {kTile128Two, 128, 128, 512, 2.5, 1.1},
-      {kTile256, 256, 256, 256, 21.0, 1.47}};
+      {kTile32x64, 32, 64, 1, 0.6, 0.13, 0.20}, {kTile64, 64, 64, 1, 1.2, 0.195, 0.22},
+      {kTile64x128, 64, 128, 1, 3.0, 0.33, 0},  {kTile128, 128, 128, 1, 4.6, 0.56, 0},
+      {kTile128Two, 128, 128, 2, 3.25, 0.55, 0}, {kTile256, 256, 256, 1, 18.0, 1.45, 0}};
   const double stages = (a.K + 127) / 128;
   const int64_t ld = ((int64_t)a.K + 15) / 16 * 16;
   const double moved = 2.0 * ((q16 ? 0 : a.S * ld) + (w16 ? 0 : a.N * ld));
@@ -515,7 +516,8 @@ QmmPlan plan_of(const QmmArgs &a) {
   }
   for (const Tile &t : kTiles) {
     const double tiles = (double)((a.N + t.n - 1) / t.n) * ((a.S + t.s - 1) / t.s);
-    const double us = copy + std::ceil(tiles / t.slots) * (t.once + t.stage * stages);
+    const double rounds = std::ceil(tiles / (256 * t.together)) * t.together;
+    const double us = copy + 1.5 + std::max(rounds * (t.once + t.stage * stages), t.alone * stages);
     if (us < best) {
       best = us;
       p.kernel = t.kernel;
