@@ -485,10 +485,10 @@ struct QmmPlan {
   int64_t bytes_q, bytes;  // workspace: of the token rows, of all
 };
 
-// The kernel with the least estimated time, from times measured over 50 shapes (us).  A
-// tile kernel: 1.5, and for each round of 256 tiles (one a compute unit) a part for its
+// The kernel with the least estimated time, from times measured over 60 shapes (us).  A
+// tile kernel: 2.5, and for each round of 256 tiles (one a compute unit) a part for its
 // start and end and a part for every 128 of K (both with `together` tiles on a unit), or the time in which one tile alone gets
-// through K.  The direct kernel: 2.7, and each workgroup moves 39 KB/us.
+// through K.  The direct kernel: 2.3, and each workgroup moves 39 KB/us.
 QmmPlan plan_of(const QmmArgs &a) {
   QmmPlan p{};
   const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);
@@ -498,8 +498,8 @@ QmmPlan plan_of(const QmmArgs &a) {
   }
   struct Tile { QmmKernel kernel; int n, s, together; double once, stage, alone; };
   static constexpr Tile kTiles[] = {
-      {kTile32x64, 32, 64, 1, 0.6, 0.13, 0.20}, {kTile64, 64, 64, 1, 1.2, 0.195, 0.22},
-      {kTile64x128, 64, 128, 1, 3.0, 0.33, 0},  {kTile128, 128, 128, 1, 4.6, 0.56, 0},
+      {kTile32x64, 32, 64, 1, 0.6, 0.13, 0.17}, {kTile64, 64, 64, 1, 1.2, 0.195, 0.18},
+      {kTile64x128, 64, 128, 1, 3.0, 0.33, 0.22},  {kTile128, 128, 128, 1, 4.6, 0.56, 0},
       {kTile128Two, 128, 128, 2, 3.25, 0.55, 0}, {kTile256, 256, 256, 1, 18.0, 1.45, 0}};
   const double stages = (a.K + 127) / 128;
   const int64_t ld = ((int64_t)a.K + 15) / 16 * 16;
@@ -508,7 +508,7 @@ QmmPlan plan_of(const QmmArgs &a) {
   double best = 1e30;
   for (int nt = 1; nt <= 2; ++nt) {
     const double groups = (double)((a.N + 15) / 16) * ((a.S + 16 * nt - 1) / (16 * nt));
-    const double t = 2.7 + std::max(1.0, groups / 256) * 16 * (1 + nt) * a.K / 39e3;
+    const double t = 2.3 + std::max(1.0, groups / 256) * 16 * (1 + nt) * a.K / 39e3;
     if (t < best && groups <= 1 << 18) {
       best = t;
       p.kernel = nt == 1 ? kFew1 : kFew2;
@@ -517,7 +517,7 @@ QmmPlan plan_of(const QmmArgs &a) {
   for (const Tile &t : kTiles) {
     const double tiles = (double)((a.N + t.n - 1) / t.n) * ((a.S + t.s - 1) / t.s);
     const double rounds = std::ceil(tiles / (256 * t.together)) * t.together;
-    const double us = copy + 1.5 + std::max(rounds * (t.once + t.stage * stages), t.alone * stages);
+    const double us = copy + 2.5 + std::max(rounds * (t.once + t.stage * stages), t.alone * stages);
     if (us < best) {
       best = us;
       p.kernel = t.kernel;
@@ -624,7 +624,9 @@ hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
       c.d += s;
       c.dw += n;
       c.y = (char *)a.y + (s * a.ldy + n) * (a.y_bf16 ? 2 : 4);
-      ProfScope ps(p.kernel <= kFew2 ? "qmatmul_direct" : "qmatmul_tile", st);
+      static constexpr const char *kNames[] = {"qmatmul_vec", "qmatmul_few", "qmatmul_few32", "qmatmul_tile32x64", "qmatmul_tile64",
+                                               "qmatmul_tile64x128", "qmatmul_tile128", "qmatmul_tile128x2", "qmatmul_tile256"};
+      ProfScope ps(kNames[p.kernel], st);
       launch_piece(c, p.kernel, st);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
