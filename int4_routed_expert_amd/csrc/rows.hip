@@ -360,17 +360,20 @@ void launch_held(const RowArgs &a, hipStream_t st) {
   const int xs = BF16 ? 2 : 4;
   const bool vec = on16(a.x, a.ldx, xs) && on16(a.residual, a.ldr, xs) && on16(a.h, a.ldh, xs) &&
                    on16(a.y, a.ldy, a.y_bf16 ? 2 : 4) && on16(a.gamma, 0, 1) && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0;
-  // Few rows: 8 elements a thread, since a row's latency counts (one row of 6144: 4.5 us at
-  // 12 waves, 5.3 at 4, 5.5 at 16).  Many: longer runs a thread where they measured faster
-  // (8192 x 4096: norm 63 us at 4 waves, 69 at 8; SwiGLU 36 and 45).
+  // The fewest registers that hold the row keep the most rows in flight; among the ways to
+  // split it the measured order (bf16, rows of 100 MB in all, us): 1024 wide: norm 47 at 1 x
+  // 2 (W x IT), SwiGLU 28, 47 and 32 at 2 x 1; 2048: norm 46 at 4 x 1, 47 at 2 x 2, SwiGLU 32
+  // and 28; 4096: 49 and 28 at 4 x 2, 50 and 33 at 8 x 1; 6144: 51 and 36 at 12 x 1, 57 and
+  // 31 at 4 x 3; 8192: 53 and 28 at 8 x 2, 59 and 35 at 16 x 1.  Of few rows the latency
+  // counts: one of 6144 takes 4.5 us at 12 x 1, 4.9 at 8 x 2, 5.3 at 4 x 3, 5.5 at 16 x 1.
   constexpr bool norm = OP == kNorm;
-  const bool few = a.S <= 512;
+  const bool few = a.S <= 64;
   if (a.H <= 512) launch_one<OP, BF16, 1, 1>(a, vec, st);
-  else if (a.H <= 1024 && !few) launch_one<OP, BF16, 1, 2>(a, vec, st);
-  else if (a.H <= 2048) few ? launch_one<OP, BF16, 4, 1>(a, vec, st) : launch_one<OP, BF16, 1, 4>(a, vec, st);
+  else if (a.H <= 1024) few ? launch_one<OP, BF16, 2, 1>(a, vec, st) : launch_one<OP, BF16, 1, 2>(a, vec, st);
+  else if (a.H <= 2048) few || norm ? launch_one<OP, BF16, 4, 1>(a, vec, st) : launch_one<OP, BF16, 2, 2>(a, vec, st);
   else if (a.H <= 4096) few ? launch_one<OP, BF16, 8, 1>(a, vec, st) : launch_one<OP, BF16, 4, 2>(a, vec, st);
   else if (a.H <= 6144) few || norm ? launch_one<OP, BF16, 12, 1>(a, vec, st) : launch_one<OP, BF16, 4, 3>(a, vec, st);
-  else if (a.H <= 8192) few || norm ? launch_one<OP, BF16, 8, 2>(a, vec, st) : launch_one<OP, BF16, 4, 4>(a, vec, st);
+  else if (a.H <= 8192) launch_one<OP, BF16, 8, 2>(a, vec, st);
   else if (a.H <= 12288) launch_one<OP, BF16, 12, 2>(a, vec, st);
   else if (a.H <= 16384) few || norm ? launch_one<OP, BF16, 16, 2>(a, vec, st) : launch_one<OP, BF16, 8, 4>(a, vec, st);
   else MOE_LAUNCH((k_rows_long<OP, BF16>), dim3((unsigned)std::min(a.S, 1 << 20)), dim3(kRowThreads), 0, st, a);
