@@ -418,7 +418,7 @@ int moe_pool_check_view(const moe_pool *pool, int32_t layer, const moe_slot_view
  * [H] of g_dtype.  residual may be NULL (h = x); h, y and the pair q, d may each be NULL,
  * not all of them, and h needs a residual.  h may be residual or x, and y may be x, at
  * the same stride (in place).  eps >= 0.  Statistics are fp32, added up in an order that
- * depends on H and the rows' alignment alone: a row's bits do not depend on the batch. */
+ * depends on H alone: a row's bits do not depend on the batch or on where it lies. */
 int moe_norm_quant(const void *x, int32_t x_dtype, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
                    int32_t g_dtype, float eps, int32_t S, int32_t H, void *h, int64_t ldh, void *y, int32_t y_dtype,
                    int64_t ldy, int8_t *q, int64_t ldq, float *d, void *stream);

@@ -114,70 +114,89 @@ __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
 
 // ---- rows held in registers ----------------------------------------------------------
 // A row belongs to W waves and stays in their registers between the passes.  Iteration it
-// of wave w holds the row's block it W + w of 512 elements, 8 a lane: neighbours, moved in
-// 16-byte pieces, where every row is 16-byte aligned (VEC), else 64 apart, so that a wave
-// meets 64 neighbours at a time.
-template <int W, bool VEC>
-__device__ inline int col_of(int tid, int it, int j) {
-  const int block = (it * W + (tid >> 6)) * 512, lane = tid & 63;
-  return VEC ? block + lane * 8 + j : block + j * 64 + lane;
+// of wave w holds the row's block it W + w of 512 elements, 8 neighbours a lane, moved in
+// 16-byte pieces.  ON16: every row starts at a multiple of 16 bytes (8 for the int8 rows).
+template <int W>
+__device__ inline int col_of(int tid, int it) {
+  return (it * W + (tid >> 6)) * 512 + (tid & 63) * 8;
 }
 
-// Eight neighbours of a 16-byte aligned row.
-template <bool BF16>
+typedef u32x4_t u32x4_w __attribute__((aligned(4)));
+typedef u32x4_t u32x4_h __attribute__((aligned(2)));
+typedef f32x4_t f32x4_w __attribute__((aligned(4)));
+typedef uint64_t u64_b __attribute__((aligned(1)));
+
+// Eight neighbours.  A bf16 row that starts in the middle of a word is read as the words
+// that hold the eight (each holds at least one of them), shifted together: loads from
+// odd places take the hardware several times as long.
+template <bool BF16, bool ON16>
 __device__ inline void load8(const void *p, int64_t i, float *v) {
   if constexpr (BF16) {
-    const uint4 r = ldg<uint4>((const uint16_t *)p + i);
-    const uint32_t d[4] = {r.x, r.y, r.z, r.w};
+    const uint16_t *q = (const uint16_t *)p + i;
+    uint32_t d[4];
+    if constexpr (ON16) {
+      const uint4 r = ldg<uint4>(q);
+      d[0] = r.x; d[1] = r.y; d[2] = r.z; d[3] = r.w;
+    } else {
+      const uint32_t sh = (uint32_t)(uintptr_t)q & 2;
+      const u32x4_t r = *(const __attribute__((address_space(1))) u32x4_w *)((uintptr_t)q & ~(uintptr_t)3);
+      const uint32_t e = ldg<uint32_t>((const void *)((uintptr_t)(q + 7) & ~(uintptr_t)3));
+      d[0] = __builtin_amdgcn_alignbyte(r.y, r.x, sh);
+      d[1] = __builtin_amdgcn_alignbyte(r.z, r.y, sh);
+      d[2] = __builtin_amdgcn_alignbyte(r.w, r.z, sh);
+      d[3] = __builtin_amdgcn_alignbyte(e, r.w, sh);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(d[j] << 16);
       v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
     }
   } else {
-    const float4 r0 = ldg<float4>((const float *)p + i), r1 = ldg<float4>((const float *)p + i + 4);
-    v[0] = r0.x; v[1] = r0.y; v[2] = r0.z; v[3] = r0.w;
-    v[4] = r1.x; v[5] = r1.y; v[6] = r1.z; v[7] = r1.w;
+    const float *q = (const float *)p + i;
+    const f32x4_t r0 = *(const __attribute__((address_space(1))) f32x4_w *)q;
+    const f32x4_t r1 = *(const __attribute__((address_space(1))) f32x4_w *)(q + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = r0[j];
+      v[4 + j] = r1[j];
+    }
   }
 }
-template <bool BF16>
+template <bool BF16, bool ON16>
 __device__ inline void store8(void *p, int64_t i, const float *v) {
   if constexpr (BF16) {
-    uint32_t d[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
-    stg<uint4>((uint16_t *)p + i, make_uint4(d[0], d[1], d[2], d[3]));
+    const u32x4_t d = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
+    uint16_t *q = (uint16_t *)p + i;
+    if constexpr (ON16) *(__attribute__((address_space(1))) u32x4_t *)q = d;
+    else *(__attribute__((address_space(1))) u32x4_h *)q = d;
   } else {
-    stg<float4>((float *)p + i, make_float4(v[0], v[1], v[2], v[3]));
-    stg<float4>((float *)p + i + 4, make_float4(v[4], v[5], v[6], v[7]));
+    float *q = (float *)p + i;
+    *(__attribute__((address_space(1))) f32x4_w *)q = f32x4_t{v[0], v[1], v[2], v[3]};
+    *(__attribute__((address_space(1))) f32x4_w *)(q + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
   }
 }
 
 // The 8 elements of iteration it, those below H (others are left alone).
-template <int W, bool VEC, bool BF16>
+template <int W, bool ON16, bool BF16>
 __device__ inline void load_it(const void *p, int64_t row, int H, int tid, int it, float *v) {
-  const int c = col_of<W, VEC>(tid, it, 0);
-  if (VEC && c + 8 <= H) {
-    load8<BF16>(p, row + c, v);
+  const int c = col_of<W>(tid, it);
+  if (c + 8 <= H) {
+    load8<BF16, ON16>(p, row + c, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = col_of<W, VEC>(tid, it, j);
-      if (k < H) v[j] = load_el<BF16>(p, row + k);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (c + j < H) v[j] = load_el<BF16>(p, row + c + j);
   }
 }
-template <int W, bool VEC, bool BF16>
+template <int W, bool ON16, bool BF16>
 __device__ inline void store_it(void *p, int64_t row, int H, int tid, int it, const float *v) {
-  const int c = col_of<W, VEC>(tid, it, 0);
-  if (VEC && c + 8 <= H) {
-    store8<BF16>(p, row + c, v);
+  const int c = col_of<W>(tid, it);
+  if (c + 8 <= H) {
+    store8<BF16, ON16>(p, row + c, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = col_of<W, VEC>(tid, it, j);
-      if (k < H) store_el<BF16>(p, row + k, v[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (c + j < H) store_el<BF16>(p, row + c + j, v[j]);
   }
 }
 
@@ -230,7 +249,7 @@ struct Codes {
   }
 };
 
-template <RowOp OP, bool BF16, int W, int IT, bool VEC>
+template <RowOp OP, bool BF16, int W, int IT, bool ON16>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
   // each row of a workgroup's turn uses the other half, so one barrier orders both uses
   __shared__ __align__(16) float s_sum[2][W * IT];
@@ -242,10 +261,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
        r += (int64_t)gridDim.x * kRowsAtOnce, turn ^= 1) {
     float v[IT][8] = {}, o[IT][8] = {};
 #pragma unroll
-    for (int it = 0; it < IT; ++it) load_it<W, VEC, BF16>(a.x, r * a.ldx, a.H, tid, it, v[it]);
+    for (int it = 0; it < IT; ++it) load_it<W, ON16, BF16>(a.x, r * a.ldx, a.H, tid, it, v[it]);
     if (OP == kSilu || a.residual) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it) load_it<W, VEC, BF16>(a.residual, r * a.ldr, a.H, tid, it, o[it]);
+      for (int it = 0; it < IT; ++it) load_it<W, ON16, BF16>(a.residual, r * a.ldr, a.H, tid, it, o[it]);
     }
     if constexpr (OP == kNorm) {
       // gamma is requested with the row where the registers allow it, else after the sum
@@ -254,10 +273,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
       auto load_gamma = [&] {
         if (a.g_bf16) {
 #pragma unroll
-          for (int it = 0; it < IT; ++it) load_it<W, VEC, true>(a.gamma, 0, a.H, tid, it, g[it]);
+          for (int it = 0; it < IT; ++it) load_it<W, ON16, true>(a.gamma, 0, a.H, tid, it, g[it]);
         } else {
 #pragma unroll
-          for (int it = 0; it < IT; ++it) load_it<W, VEC, false>(a.gamma, 0, a.H, tid, it, g[it]);
+          for (int it = 0; it < IT; ++it) load_it<W, ON16, false>(a.gamma, 0, a.H, tid, it, g[it]);
         }
       };
       if constexpr (kEarly) load_gamma();
@@ -274,7 +293,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
           part[it] = fmaf(v[it][j], v[it][j], part[it]);
         }
         part[it] = wave_sum(part[it]);
-        if (a.h) store_it<W, VEC, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it]);
+        if (a.h) store_it<W, ON16, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it]);
       }
       float sum = 0.f;
       if constexpr (W > 1) {
@@ -304,8 +323,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
     if (a.y) {
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        if (a.y_bf16) store_it<W, VEC, true>(a.y, r * a.ldy, a.H, tid, it, v[it]);
-        else store_it<W, VEC, false>(a.y, r * a.ldy, a.H, tid, it, v[it]);
+        if (a.y_bf16) store_it<W, ON16, true>(a.y, r * a.ldy, a.H, tid, it, v[it]);
+        else store_it<W, ON16, false>(a.y, r * a.ldy, a.H, tid, it, v[it]);
       }
     }
     if (a.q) {
@@ -329,15 +348,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const uint32_t w[2] = {c.four(v[it]), c.four(v[it] + 4)};
-        const int k = col_of<W, VEC>(tid, it, 0);
-        if (VEC && k + 8 <= a.H) {
-          *(__attribute__((address_space(1))) uint64_t *)(a.q + r * a.ldq + k) = ((uint64_t)w[1] << 32) | w[0];
+        const int k = col_of<W>(tid, it);
+        int8_t *to = a.q + r * a.ldq + k;
+        if (k + 8 <= a.H) {
+          const uint64_t both = ((uint64_t)w[1] << 32) | w[0];
+          if constexpr (ON16) *(__attribute__((address_space(1))) uint64_t *)to = both;
+          else *(__attribute__((address_space(1))) u64_b *)to = both;
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int kj = col_of<W, VEC>(tid, it, j);
-            if (kj < a.H) stg<int8_t>(a.q + r * a.ldq + kj, (int8_t)(w[j >> 2] >> (8 * (j & 3))));
-          }
+          for (int j = 0; j < 8; ++j)
+            if (k + j < a.H) stg<int8_t>(to + j, (int8_t)(w[j >> 2] >> (8 * (j & 3))));
         }
       }
     }

@@ -325,7 +325,7 @@ def test_product_into_wider_rows(M):
 ROPE = [  # S, heads, kheads, D, rot, offset
     (1, 1, 0, 2, 2, 0), (1, 64, 1, 64, 64, 0), (8, 64, 8, 128, 128, 0), (3, 5, 2, 20, 12, 3), (7, 24, 3, 192, 64, 128),
     (33, 3, 1, 80, 32, 0), (130, 1, 1, 64, 64, 0), (130, 1, 0, 64, 16, 48), (9, 2, 2, 1024, 1024, 0), (5, 9, 4, 96, 48, 24),
-    (300, 16, 4, 128, 128, 0), (4, 1000, 1, 64, 32, 32), (1000, 2, 1, 36, 36, 0), (1500, 1, 1, 256, 64, 64),
+    (300, 16, 4, 128, 128, 0), (50, 7, 3, 72, 40, 4), (50, 6, 2, 68, 68, 0), (21, 3, 1, 44, 20, 24), (4, 1000, 1, 64, 32, 32), (1000, 2, 1, 36, 36, 0), (1500, 1, 1, 256, 64, 64),
 ]
 
 
@@ -510,6 +510,22 @@ def test_rows_do_not_depend_on_the_batch(M, H, dtype):
         few = M.norm_quant(x[lo:hi], gamma, 1e-5, residual=r[lo:hi], y_dtype=BF) + M.silu_quant(x[lo:hi], r[lo:hi], y_dtype=BF)
         for a, b in zip(many, few):
             assert torch.equal(a[lo:hi], b)
+
+
+@pytest.mark.parametrize("H", [77, 1000, 6144])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_do_not_depend_on_where_they_lie(M, H, dtype):
+    """The same rows at other offsets and distances give the same bits."""
+    x = rows(rng(H), 9, H, dtype)
+    gamma = torch.rand(H, device="cuda", generator=rng(1))
+    want = M.norm_quant(x, gamma, 1e-5, residual=x, y_dtype=dtype) + M.silu_quant(x, x, y_dtype=dtype)
+    for pad, start in ((1, 0), (0, 1), (3, 5), (8, 2), (16, 8)):
+        buf = torch.full((start + 9 * (H + pad),), float("nan"), dtype=dtype, device="cuda")
+        z = buf[start:].view(9, H + pad)[:, :H]
+        z.copy_(x)
+        got = M.norm_quant(z, gamma, 1e-5, residual=z, y_dtype=dtype) + M.silu_quant(z, z, y_dtype=dtype)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
 
 
 def test_same_rule_as_the_layers_int8_activations(M):
