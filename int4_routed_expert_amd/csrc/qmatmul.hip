@@ -1,5 +1,15 @@
 // Product of int8 rows with int8 weights: y[s, n] = (sum_k q[s, k] w[n, k]) * (d[s] * dw[n]),
-// the sum exact in int32.
+// the sum exact in int32, scaled once in fp32.  Three kernels, chosen by estimated time
+// (plan_of): a dot-product kernel for up to four tokens, a direct matrix-core kernel for
+// few tokens or small operands, LDS tiles for the others.  Measured (bf16 outputs):
+//   1 x 4096 x 6144 (S x N x K)   5.8 us, 4.3 TB/s; 1 x 12288 x 6144 12.4 us, 6.1 TB/s (a
+//                                 copy of 1 GiB runs at 5.1): bound by the weights' bytes
+//   256 x 6144 x 6144             18 us, 1.07 POP/s: a compute unit takes in about 80 KB/us
+//                                 past its XCD's L2, and the tiles move 1.2 MB through each
+//   8192 x 12288 x 6144           546 us, 2.27 POP/s (a library int8 product: 2.04): the
+//                                 matrix cores are busy 61% of the cycles, and the chip
+//                                 clocks down to 1.8 GHz to stay within its power (all
+//                                 operands zero: 484 us)
 #include <algorithm>
 #include <cmath>
 
@@ -167,11 +177,12 @@ __global__ __launch_bounds__(256) void k_qmm_vec(QmmArgs a) {
   }
 }
 
-// ---- few tokens ------------------------------------------------------------------
-// A workgroup takes 16 MT weight rows and all the tokens (NT blocks of 16); its waves
-// split K and add their int32 sums in LDS.  v_mfma_i32_16x16x64_i8 with the weights as
-// rows and the tokens as columns, both operands straight from memory: lane l holds 16
-// bytes of row (or token) l % 16 at k + 16 (l / 16).
+// ---- few tokens or small operands -----------------------------------------------------
+// A workgroup takes 16 MT weight rows and 16 NT tokens; its W waves split K and add their
+// int32 sums in LDS.  v_mfma_i32_16x16x64_i8 with the weights as rows and the tokens as
+// columns, both operands straight from memory: lane l holds 16 bytes of row (or token) l %
+// 16 at k + 16 (l / 16).  Nothing is staged, so a small product ends after little more
+// than one trip to memory (77 x 577 x 1111: 4.2 us; tiles 6.5 and the copies before them).
 template <int MT, int NT, int W, bool W4>
 __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
   constexpr int kU = MT * NT >= 4 ? 2 : 4;  // k steps in flight
@@ -252,22 +263,23 @@ __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
 }
 
 // ---- many tokens -----------------------------------------------------------------
-// A workgroup of WN x WS waves takes BN weight rows x BS tokens, each wave its
-// (BN / WN) x (BS / WS) part in blocks of v_mfma_i32_32x32x32_i8 (weights as rows, tokens
-// as columns).  Both operands go through LDS in stages of 64 bytes of K, NBUF of them:
-// stage s + NBUF is requested as soon as stage s has been read.
+// A workgroup takes BN weight rows x BS tokens; WN x WS waves each their (BN / WN) x (BS /
+// WS) part in blocks of v_mfma_i32_32x32x32_i8 (weights as rows, tokens as columns).  Both
+// operands go through LDS in stages of kBK bytes of K, NBUF of them: a stage's buffer is
+// requested anew as soon as the stage has been read.  KS teams of such waves may share a
+// tile, each with every KS-th stage, and add up at the end.  Stages of 128 bytes of K: a
+// row of a stage is a whole cache line (rows of 64 bytes reach 64 KB/us a compute unit out
+// of L2, rows of 128 120).  The 256 x 256 tile gives a wave 128 x 128 outputs, 256
+// accumulators a lane, so that reading LDS takes half the matrix cores' time; smaller
+// tiles spread smaller products over the chip.
 constexpr int kXcds = 8;
 
 // Where the 16-byte chunk c of a stage's row r lies: the rows' chunks are permuted so that
-// lanes reading one chunk of neighbouring rows spread over the banks.
-template <int BK>
-__device__ inline int mix_of(int r) {
-  return BK == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
-}
-template <int BK>
-__device__ inline int chunk_of(int r, int c) {
-  return r * BK + ((c ^ mix_of<BK>(r)) << 4);
-}
+// lanes reading one chunk of 16 neighbouring rows spread over all banks (no conflicts are
+// counted; permuted over 8 rows, 8192 x 12288 x 6144 took 611 us where this took 597).
+constexpr int kBK = 128;
+__device__ inline int mix_of(int r) { return (r >> 1) & 7; }
+__device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ mix_of(r)) << 4); }
 
 // One 16-byte load per lane from p straight into LDS, to lds + off + 16 lane (lds
 // wave-uniform, off a constant).
@@ -281,18 +293,23 @@ __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int BN, int BS, int WN, int WS, int kBK, int NBUF>
-__global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
-  constexpr int kThr = 64 * WN * WS;
+template <int BN, int BS, int WN, int WS, int NBUF, int KS>
+__global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
+  constexpr int kThr = 64 * WN * WS;  // of one of the KS teams
   constexpr int TN = BN / WN / 32, TS = BS / WS / 32;  // 32x32 blocks of a wave
   constexpr int kRows = BN + BS, kStage = kRows * kBK;
   constexpr int kPer = kStage / 16 / kThr;  // chunks a thread moves per stage
   static_assert(kStage % (16 * kThr) == 0, "stage split");
   constexpr int kWide = BN / WN, kLd = kWide + 4;  // a wave's weights, and what a token's sums of them take in LDS
   constexpr int kTurn = WN * WS * 32 * kLd * 4, kEnd = kTurn + kRows * 4;
-  __shared__ __align__(128) uint8_t s_buf[NBUF * kStage > kEnd ? NBUF * kStage : kEnd];
-  float *s_sc = (float *)(s_buf + kTurn);  // after the last stage: the weights' scales, then the tokens'
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kSums = KS > 1 ? (KS - 1) * BN * BS * 4 : 0;  // the other teams' sums
+  constexpr int kLds = std::max({KS * NBUF * kStage, kEnd, kSums});
+  __shared__ __align__(128) uint8_t s_all[kLds];
+  const int lane = threadIdx.x & 63;
+  const int team = KS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThr) : 0;
+  const int tid = threadIdx.x - team * kThr, wave = tid >> 6;
+  uint8_t *s_buf = s_all + team * NBUF * kStage;
+  float *s_sc = (float *)(s_all + kTurn);  // after the last stage: the weights' scales, then the tokens'
   const int wn = wave / WS, wsv = wave % WS;
 
   // Blocks go to the XCDs round-robin; each XCD gets a contiguous run of tiles, ordered in
@@ -306,18 +323,18 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   const int ts = strip * group + in % g, tn = in / g;
   const int n0 = tn * BN, s0 = ts * BS;
 
-  // this thread's chunks of a stage: LDS position threadIdx.x + i kThr, which holds chunk
-  // c of row r
+  // this thread's chunks of a stage: LDS position tid + i kThr, which holds chunk c of row r
   const int8_t *src[kPer];
   int kc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     constexpr int kC = kBK / 16;  // chunks of a row
-    const int p = threadIdx.x + i * kThr, r = p / kC;
-    kc[i] = ((p % kC) ^ mix_of<kBK>(r)) << 4;
+    const int p = tid + i * kThr, r = p / kC;
+    kc[i] = ((p % kC) ^ mix_of(r)) << 4;
     src[i] = r < BN ? a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw : a.q + (int64_t)min(s0 + r - BN, a.S - 1) * a.ldq;
   }
-  const int stages = (a.K + kBK - 1) / kBK;
+  // a team takes every KS-th stage of K; beyond K its stages are zeros
+  const int stages = (a.K + KS * kBK - 1) / (KS * kBK);
   const int whole = a.K / kBK;
 
   i32x16 acc[TN][TS];
@@ -335,8 +352,8 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   int at_w[kSteps], at_t[kSteps];
 #pragma unroll
   for (int kk = 0; kk < kSteps; ++kk) {
-    at_w[kk] = chunk_of<kBK>(wn * (BN / WN) + row, kk * 2 + ck);
-    at_t[kk] = chunk_of<kBK>(BN + wsv * (BS / WS) + row, kk * 2 + ck);
+    at_w[kk] = chunk_of(wn * (BN / WN) + row, kk * 2 + ck);
+    at_t[kk] = chunk_of(BN + wsv * (BS / WS) + row, kk * 2 + ck);
   }
   // fragment f of a k step: the wave's TN weight blocks, then its TS token blocks
   auto frag = [&](const uint8_t *buf, int f, int kk) __attribute__((always_inline)) {
@@ -352,30 +369,35 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) src[i] += kc[i];
+  for (int i = 0; i < kPer; ++i) src[i] += kc[i] + team * kBK;
   auto clip = [&](int s) __attribute__((always_inline)) {  // before stage s is requested
-    if (s >= whole) {
+    const int at = s * KS + team;
+    if (at >= whole) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if ((int64_t)s * kBK + kc[i] >= a.K) src[i] = (const int8_t *)g_zeros;
+        if ((int64_t)at * kBK + kc[i] >= a.K) src[i] = (const int8_t *)g_zeros;
     }
   };
   auto request = [&](int i, int buffer) __attribute__((always_inline)) {
     load_to_lds(src[i], lds, buffer * kStage + i * kThr * 16);
-    src[i] += kBK;
+    src[i] += KS * kBK;
   };
+  // Fragments are read a group of kG k steps ahead, at least 4 MFMAs: they take longer to
+  // arrive than one MFMA takes.
+  constexpr int kG = kM >= 8 ? 1 : kM >= 4 ? 2 : 4, kGroups = kSteps / kG;
+  static_assert(kSteps % kG == 0 && NBUF % 2 == 0, "groups of k steps");
+  // A stage's new requests go out over its own last group and the first of the next stage:
+  // all in one group they wait for each other (8192x12288x6144: 582 us, 558 over two, 571
+  // over four, where the last arrive late).
+  constexpr int kSpread = kGroups > 1 ? 2 : 1;
 #pragma unroll
   for (int s = 0; s < NBUF; ++s) {
     clip(s);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) request(i, s);
+    for (int i = 0; i < (s < NBUF - 1 ? kPer : kPer / kSpread); ++i) request(i, s);
   }
-  wait_loads<0>();
+  wait_loads<(NBUF - 2) * kPer + kPer / kSpread>();
   __builtin_amdgcn_s_barrier();
-  // Fragments are read a group of kG k steps ahead, at least 4 MFMAs: they take longer to
-  // arrive than one MFMA takes.
-  constexpr int kG = kM >= 4 ? (kM >= 8 ? 1 : 2) : kSteps < 4 ? kSteps : 4, kGroups = kSteps / kG;
-  static_assert(kSteps % kG == 0 && NBUF % 2 == 0, "groups of k steps");
   i32x4 F[2][kG][kF];
 #pragma unroll
   for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
@@ -396,10 +418,6 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // A stage's new requests go out over its own last group and the first of the next stage:
-  // all in one group they wait for each other (8192x12288x6144: 582 us, 558 over two, 571
-  // over four, where the last arrive late).
-  constexpr int kSpread = kGroups > 1 ? 2 : 1;
   auto stage = [&](int s, int b) __attribute__((always_inline)) {  // stage s, in buffer b
     const int cur = b * kGroups & 1;
 #pragma unroll
@@ -411,9 +429,6 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
     clip(s + NBUF);
     multiply((cur + kGroups - 1) & 1, (b + 1) % NBUF, 0, b, 0, kPer / kSpread);
   };
-  // what the first stage's groups would request of the one before it has been requested
-#pragma unroll
-  for (int i = kPer / kSpread; i < kPer; ++i) src[i] -= kBK;
   int s = 0;
   for (; s + NBUF <= stages; s += NBUF) {
 #pragma unroll
@@ -424,12 +439,38 @@ __global__ __launch_bounds__(64 * WN * WS) void k_qmm_tile(QmmArgs a, int tiles_
     if (s + b < stages) stage(s + b, b);
   wait_loads<0>();
 
+  __syncthreads();
+  if constexpr (KS > 1) {  // the first team adds the others' sums to its own
+    i32x4 *sums = (i32x4 *)s_all;
+    constexpr int kAcc = TN * TS * 4;  // pieces of four of a lane
+    auto piece = [&](int t, int c) { return ((t - 1) * kAcc + c) * kThr + tid; };
+    if (team) {
+#pragma unroll
+      for (int c = 0; c < kAcc; ++c) {
+        const i32x16 &v = acc[c / 4 / TS][c / 4 % TS];
+        sums[piece(team, c)] = i32x4{v[c % 4 * 4], v[c % 4 * 4 + 1], v[c % 4 * 4 + 2], v[c % 4 * 4 + 3]};
+      }
+    }
+    __syncthreads();
+    if (!team) {
+#pragma unroll
+      for (int t = 1; t < KS; ++t)
+#pragma unroll
+        for (int c = 0; c < kAcc; ++c) {
+          const i32x4 v = sums[piece(t, c)];
+          i32x16 &to = acc[c / 4 / TS][c / 4 % TS];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[c % 4 * 4 + e] += v[e];
+        }
+    }
+    __syncthreads();
+  }
   // Each wave turns its sums round in its own part of the buffers, 32 tokens at a time, so
   // that they leave as runs of a token's neighbouring outputs.
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRows; i += kThr)
+  for (int i = threadIdx.x; i < kRows; i += KS * kThr)
     s_sc[i] = i < BN ? ldg<float>(a.dw + min(n0 + i, a.N - 1)) : ldg<float>(a.d + min(s0 + i - BN, a.S - 1));
   __syncthreads();
+  if (team) return;
   int *out = (int *)s_buf + wave * 32 * kLd;
   constexpr int kRun = kWide / 4, kTok = 64 / kRun;  // lanes of a token's run, tokens at a time
 #pragma unroll
@@ -473,7 +514,7 @@ __global__ __launch_bounds__(256) void k_qmm_align(QmmArgs a, int8_t *q, int8_t 
 }
 
 // ---- which kernel --------------------------------------------------------------------
-enum QmmKernel { kVec, kFew1, kFew2, kTile32x64, kTile64, kTile64x128, kTile128, kTile128Two, kTile256 };
+enum QmmKernel { kVec, kFew1, kFew2, kTile32, kTile32x64, kTile64, kTile64x128, kTile128, kTile128Two, kTile256 };
 
 bool on16(const int8_t *p, int64_t ld, int rows, int K) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && K % 16 == 0;
@@ -498,6 +539,7 @@ QmmPlan plan_of(const QmmArgs &a) {
   }
   struct Tile { QmmKernel kernel; int n, s, together; double once, stage, alone; };
   static constexpr Tile kTiles[] = {
+      {kTile32, 32, 32, 1, 1.1, 0.083, 0.095},
       {kTile32x64, 32, 64, 1, 0.6, 0.13, 0.17}, {kTile64, 64, 64, 1, 1.2, 0.195, 0.18},
       {kTile64x128, 64, 128, 1, 3.0, 0.33, 0.22},  {kTile128, 128, 128, 1, 4.6, 0.56, 0},
       {kTile128Two, 128, 128, 2, 3.25, 0.55, 0}, {kTile256, 256, 256, 1, 18.0, 1.45, 0}};
@@ -523,7 +565,7 @@ QmmPlan plan_of(const QmmArgs &a) {
       p.kernel = t.kernel;
     }
   }
-  if (p.kernel >= kTile32x64) {
+  if (p.kernel >= kTile32) {
     p.copy_q = !q16;
     p.copy_w = !w16;
     p.bytes_q = q16 ? 0 : a.S * ld;
@@ -561,13 +603,13 @@ void launch_direct(const QmmArgs &a, QmmKernel k, hipStream_t st) {
   else launch_vec_for<4, W4>(a, st);
 }
 
-template <int BN, int BS, int WN, int WS, int BK, int NBUF>
+template <int BN, int BS, int WN, int WS, int NBUF, int KS>
 void launch_tile(const QmmArgs &a, hipStream_t st) {
   const int tn = (a.N + BN - 1) / BN, ts = (a.S + BS - 1) / BS;
   const int64_t total = (int64_t)tn * ts;
   const dim3 g((unsigned)((total + kXcds - 1) / kXcds * kXcds));
   const int group = 4;
-  MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, BK, NBUF>), g, dim3(64 * WN * WS), 0, st, a, tn, ts, group);
+  MOE_LAUNCH((k_qmm_tile<BN, BS, WN, WS, NBUF, KS>), g, dim3(64 * WN * WS * KS), 0, st, a, tn, ts, group);
 }
 
 }  // namespace
@@ -585,12 +627,13 @@ void launch_piece(const QmmArgs &a, QmmKernel kernel, hipStream_t st) {
       else launch_direct<false>(a, kernel, st);
       break;
     }
-    case kTile32x64: launch_tile<32, 64, 1, 2, 128, 4>(a, st); break;
-    case kTile64: launch_tile<64, 64, 2, 2, 128, 4>(a, st); break;
-    case kTile64x128: launch_tile<64, 128, 2, 4, 128, 4>(a, st); break;
-    case kTile128: launch_tile<128, 128, 2, 4, 128, 4>(a, st); break;
-    case kTile128Two: launch_tile<128, 128, 2, 2, 128, 2>(a, st); break;
-    case kTile256: launch_tile<256, 256, 2, 2, 128, 2>(a, st); break;
+    case kTile32: launch_tile<32, 32, 1, 1, 4, 2>(a, st); break;
+    case kTile32x64: launch_tile<32, 64, 1, 2, 4, 1>(a, st); break;
+    case kTile64: launch_tile<64, 64, 2, 2, 4, 1>(a, st); break;
+    case kTile64x128: launch_tile<64, 128, 2, 4, 4, 1>(a, st); break;
+    case kTile128: launch_tile<128, 128, 2, 4, 4, 1>(a, st); break;
+    case kTile128Two: launch_tile<128, 128, 2, 2, 2, 1>(a, st); break;
+    case kTile256: launch_tile<256, 256, 2, 2, 2, 1>(a, st); break;
   }
 }
 
@@ -624,8 +667,8 @@ hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
       c.d += s;
       c.dw += n;
       c.y = (char *)a.y + (s * a.ldy + n) * (a.y_bf16 ? 2 : 4);
-      static constexpr const char *kNames[] = {"qmatmul_vec", "qmatmul_few", "qmatmul_few32", "qmatmul_tile32x64", "qmatmul_tile64",
-                                               "qmatmul_tile64x128", "qmatmul_tile128", "qmatmul_tile128x2", "qmatmul_tile256"};
+      static constexpr const char *kNames[] = {"qmatmul_vec", "qmatmul_few", "qmatmul_few32", "qmatmul_tile32", "qmatmul_tile32x64",
+                                               "qmatmul_tile64", "qmatmul_tile64x128", "qmatmul_tile128", "qmatmul_tile128x2", "qmatmul_tile256"};
       ProfScope ps(kNames[p.kernel], st);
       launch_piece(c, p.kernel, st);
       const hipError_t e = hipGetLastError();

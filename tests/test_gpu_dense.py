@@ -260,7 +260,8 @@ def test_product(M, S, N, K, pad, start):
 
 @pytest.mark.parametrize("S,N,K,kernel", [
     (1, 500, 300, "vec"), (3, 20000, 64, "vec"), (4, 4000, 1040, "vec"), (9, 300, 1030, "few"), (64, 700, 512, "few"),
-    (130, 700, 272, "few32"), (17, 4100, 272, "few32"), (260, 1024, 528, "tile32x64"), (1540, 300, 272, "tile32x64"),
+    (130, 700, 272, "few32"), (17, 4100, 272, "few32"), (17, 4096, 4112, "tile32"), (130, 1024, 2064, "tile32"),
+    (30, 700, 16400, "tile32"), (260, 1024, 528, "tile32x64"), (1540, 300, 272, "tile32x64"),
     (770, 1024, 272, "tile64"), (48, 8208, 528, "tile64"), (200, 6160, 2064, "tile64x128"), (770, 4096, 272, "tile128"),
     (200, 12304, 272, "tile128"), (1540, 4096, 272, "tile128x2"), (2050, 6160, 1040, "tile256"), (1030, 12300, 1056, "tile256")])
 def test_every_product_kernel(M, S, N, K, kernel):
