@@ -1,5 +1,5 @@
 // C ABI of the dense operators: argument checks and host helpers.  Declarations
-// and contracts: include/moe.h.
+// and contracts: include/moe_dense.h.
 #include <algorithm>
 #include <cmath>
 

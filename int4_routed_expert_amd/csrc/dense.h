@@ -2,6 +2,7 @@
 // product, rotary positions).
 #pragma once
 
+#include "../../include/moe_dense.h"
 #include "dot.h"
 
 namespace moe {

@@ -1,4 +1,4 @@
-"""Python binding of ``libmoe.so`` (include/moe.h): argument marshalling only.
+"""Python binding of ``libmoe.so`` (include/moe.h, include/moe_dense.h): argument marshalling only.
 
 Every function with a ``moe_`` name calls the C entry point of the same name.
 Tensors are passed as raw pointers (``torch.Tensor.data_ptr()`` for device
@@ -15,7 +15,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
-HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
+HEADERS = [os.path.join(os.path.dirname(_HERE), "include", h) for h in ("moe.h", "moe_dense.h")]
 
 MOE_OK, MOE_EINVAL, MOE_ENULL, MOE_EDTYPE, MOE_EWORKSPACE, MOE_ENOSLOT, MOE_ESTALE, MOE_EHIP, MOE_ELEASE = \
     0, -1, -2, -3, -4, -5, -6, -7, -8
@@ -122,8 +122,8 @@ _lib = _load()
 
 
 def header_functions() -> list[str]:
-    """Names of the functions include/moe.h declares."""
-    text = open(HEADER).read()
+    """Names of the functions that the library's headers declare."""
+    text = "".join(open(h).read() for h in HEADERS)
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
 

@@ -176,3 +176,18 @@ def t(*shape, dtype=torch.float32):
 def test_binding_refusals(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_header_is_plain_c(tmp_path):
+    """include/moe_dense.h compiles by itself as strict C11, and its functions are exported and bound."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "t.c"
+    src.write_text('#include "moe_dense.h"\nint main(void) { moe_rope_tensor t = {0}; return t.heads + MOE_ROPE_YARN - 3; }\n')
+    subprocess.check_call(["gcc", "-std=c11", "-pedantic-errors", "-Wall", "-Wextra", "-Werror", "-I",
+                           os.path.join(root, "include"), "-c", str(src), "-o", str(tmp_path / "t.o")])
+    names = {"moe_norm_quant", "moe_silu_quant", "moe_qmatmul", "moe_qmatmul_workspace_bytes", "moe_rope", "moe_rope_freqs"}
+    assert names <= set(M.header_functions())
+    for n in names:
+        assert hasattr(L, n) and callable(getattr(M, n))
