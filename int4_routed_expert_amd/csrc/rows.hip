@@ -4,9 +4,10 @@
 //   then d = max|v| / 127 and q = rint(v / d).
 // Bound by memory: the row stays in registers between the statistics and the outputs, so
 // each input is read and each output written once (counters: 1.00 times the unique bytes).
-// Measured: norm 8192 x 6144 bf16 with residual, norm and int8 rows 97 us, 4.7 TB/s (fp32
-// in: 133 us, 5.7); SwiGLU 4096 x 12288 bf16 57 us, 4.4 TB/s (fp32: 85 us, 5.3; a copy of 1
-// GiB runs at 5.1); one row of 6144 4.4 us, two barriers and a trip to memory.
+// Measured: norm 8192 x 6144 bf16 with residual, norm and int8 rows 99 us, 4.6 TB/s (fp32
+// in: 132 us, 5.7); SwiGLU 4096 x 12288 bf16 65 us, 3.9 TB/s (fp32: 85 us, 5.3; a copy of 1
+// GiB runs at 5.1): in bf16 the exponential and the divisions take about as long as the
+// memory.  One row of 6144: 4.8 us, two barriers and a trip to memory.
 #include <algorithm>
 
 #include "dense.h"
@@ -16,22 +17,27 @@ namespace {
 
 enum RowOp { kNorm, kSilu };
 
-// exp(x) to about 2^-22: 2^t by the hardware (1 ulp) for t = x log2(e) rounded to fp32,
-// times 1 + ln 2 (x log2(e) - t), what the rounding of t dropped.
-__device__ inline float exp_near(float x) {
-  const float hi = 1.44269502f, lo = 1.92596303e-8f;  // log2(e) in two parts
-  const float t = x * hi;
-  const float rest = fmaf(x, lo, fmaf(x, hi, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e, rest * 0.693147182f, e);
-}
+// silu(g) u in the order and with the functions of the experts' SwiGLU: int8 codes come
+// out next to a rounding border the same wherever the same values are computed.  (With the
+// exponential and the quotient from the hardware's approximations SwiGLU 4096 x 12288
+// takes 57 us.)
+__device__ inline float silu_times(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// silu(g) u.  Below -88 exp would overflow and the quotient vanishes, as the true value
-// nearly does.
-__device__ inline float silu_times(float g, float u) {
-  const float e = g > -88.0f ? exp_near(fmaxf(-g, -126.0f)) : __builtin_inff();
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
-}
+// Division of many numbers by one: the product with its reciprocal and one correction
+// step, which rounds as the division does except next to a midpoint of two fp32 values
+// (three operations in place of about ten), where that neither overflows nor underflows.
+struct Divisor {
+  float d, r;
+  bool near;
+  __device__ explicit Divisor(float by) : d(by) {
+    near = d >= 0x1p-100f && d <= 0x1p100f;
+    r = __fdiv_rn(1.0f, d);
+  }
+  __device__ float fast(float v) const {  // near only
+    const float p = v * r;
+    return fmaf(fmaf(-p, d, v), r, p);
+  }
+};
 
 // v as an int8 code.  The division is IEEE fp32; a denormal scale has too few bits to
 // hold |v / d| at 127, hence the clamp.
@@ -41,13 +47,13 @@ __device__ inline int code_of(float v, float d) {
 
 constexpr int kRowThreads = 256;
 
-__device__ inline float block_sum(float v, float *s) {
+__device__ inline double block_sum(double v, double *s) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = 0.f;
+  double t = 0.;
   for (int i = 0; i < (int)blockDim.x / 64; ++i) t += s[i];
   return t;
 }
@@ -65,15 +71,19 @@ __device__ inline uint32_t block_max(uint32_t v, uint32_t *s) {
   return t;
 }
 
+// sqrt(mean + eps) from the sum of a row's squares.  Sums over lanes and waves are fp64, so
+// that the fp32 mean is nearly always the rounded one.
+__device__ inline float root_of(double sum, const RowArgs &a) { return sqrtf((float)(sum / a.H) + a.eps); }
+
 // Rows of any length: the row is read once for the statistics and again for each
 // output; a thread meets the same elements in every pass, so outputs may be inputs.
 template <RowOp OP, bool BF16>
 __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
-  __shared__ float s_sum[kRowThreads / 64];
+  __shared__ double s_sum[kRowThreads / 64];
   __shared__ uint32_t s_max[kRowThreads / 64];
   for (int64_t r = blockIdx.x; r < a.S; r += gridDim.x) {
     const int64_t xr = r * a.ldx, rr = r * a.ldr, hr = r * a.ldh, yr = r * a.ldy, qr = r * a.ldq;
-    float rstd = 1.f;
+    float root = 1.f;
     auto input = [&](int64_t c) {
       float v = load_el<BF16>(a.x, xr + c);
       if (a.residual) {
@@ -87,17 +97,17 @@ __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
         return silu_times(load_el<BF16>(a.x, xr + c), load_el<BF16>(a.residual, rr + c));
       } else {
         const float g = a.g_bf16 ? load_el<true>(a.gamma, c) : load_el<false>(a.gamma, c);
-        return (a.h ? load_el<BF16>(a.h, hr + c) : input(c)) * rstd * g;
+        return __fdiv_rn(a.h ? load_el<BF16>(a.h, hr + c) : input(c), root) * g;
       }
     };
     if constexpr (OP == kNorm) {
-      float sum = 0.f;
+      double sum = 0.;
       for (int64_t c = threadIdx.x; c < a.H; c += kRowThreads) {
         const float v = input(c);
         if (a.h) store_el<BF16>(a.h, hr + c, v);
-        sum = fmaf(v, v, sum);
+        sum = fma((double)v, (double)v, sum);
       }
-      rstd = 1.0f / sqrtf(block_sum(sum, s_sum) / (float)a.H + a.eps);
+      root = root_of(block_sum(sum, s_sum), a);
     }
     float d = 0.f;
     if (a.q) {
@@ -207,8 +217,24 @@ __device__ inline void store_it(void *p, int64_t row, int H, int tid, int it, co
 }
 
 // The wave's sum and maximum, in every lane (the row operations leave them in lane 63).
-__device__ inline float wave_sum(float v) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_to63(v)), 63));
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ inline double dpp_add(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROW_MASK, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROW_MASK, 0xF, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ inline double wave_sum(double v) {
+  v = dpp_add<0xB1>(v);        // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E>(v);        // quad_perm [2,3,0,1]
+  v = dpp_add<0x141>(v);       // row_half_mirror
+  v = dpp_add<0x140>(v);       // row_mirror
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast:15
+  v = dpp_add<0x143, 0xC>(v);  // row_bcast:31
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ inline uint32_t dpp_max(uint32_t v) {
@@ -224,22 +250,12 @@ __device__ inline uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Four values as int8 codes.  In the common range of scales v / d is the product with
-// r = 1 / d and one correction step, which rounds as the division does except next to a
-// midpoint of two fp32 values (three operations in place of about ten); adding 1.5 2^23
-// rounds to the nearest integer, ties to even, and leaves it in the low bits.
-struct Codes {
-  float d, r;
-  bool usable, near;
-  __device__ explicit Codes(float scale) : d(scale) {
-    usable = d > 0.f && d < __builtin_inff();
-    near = d >= 0x1p-100f && d <= 0x1p100f;
-    r = __fdiv_rn(1.0f, d);
-  }
-  __device__ uint32_t one(float v) const {
-    const float p = v * r;
-    return __float_as_uint(fmaf(fmaf(-p, d, v), r, p) + 12582912.0f);
-  }
+// Four values as int8 codes: adding 1.5 2^23 to v / d rounds to the nearest integer, ties
+// to even, and leaves it in the low bits.
+struct Codes : Divisor {
+  bool usable;
+  __device__ explicit Codes(float scale) : Divisor(scale) { usable = d > 0.f && d < __builtin_inff(); }
+  __device__ uint32_t one(float v) const { return __float_as_uint(fast(v) + 12582912.0f); }
   __device__ uint32_t four(const float *v) const {
     if (near) {
       const uint32_t lo = __builtin_amdgcn_perm(one(v[1]), one(v[0]), 0x0C0C0400u);
@@ -255,10 +271,12 @@ struct Codes {
   }
 };
 
+// (8 x 2: registers for three workgroups on a compute unit, 65 us against 72 for norm 4096
+// x 8192.)
 template <RowOp OP, bool BF16, int W, int IT, bool ON16>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : 1) void k_rows(RowArgs a) {
   // each row of a workgroup's turn uses the other half, so one barrier orders both uses
-  __shared__ __align__(16) float s_sum[2][W * IT];
+  __shared__ __align__(16) double s_sum[2][W * IT];
   __shared__ __align__(16) uint32_t s_max[2][W];
   constexpr int kRowsAtOnce = W == 1 ? 4 : 1;
   const int tid = W == 1 ? threadIdx.x & 63 : threadIdx.x;
@@ -286,22 +304,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
         }
       };
       if constexpr (kEarly) load_gamma();
-      // The squares of a block of 512 are summed by its wave, the blocks in their order:
-      // the same additions for every W and IT, so a row's bits do not depend on the batch.
-      float part[IT];
+      // A lane's eight squares are added in fp32, a block's 64 such sums by its wave and the
+      // blocks in their order in fp64: the same additions for every W and IT, so a row's
+      // bits do not depend on the batch.
+      double part[IT];
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        part[it] = 0.f;
+        float eight = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[it][j] += o[it][j];
           if constexpr (BF16) v[it][j] = bf16_f(f_bf16(v[it][j]));
-          part[it] = fmaf(v[it][j], v[it][j], part[it]);
+          eight = fmaf(v[it][j], v[it][j], eight);
         }
-        part[it] = wave_sum(part[it]);
+        part[it] = wave_sum((double)eight);
         if (a.h) store_it<W, ON16, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it]);
       }
-      float sum = 0.f;
+      double sum = 0.;
       if constexpr (W > 1) {
         if ((tid & 63) == 0) {
 #pragma unroll
@@ -314,12 +333,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void k_rows(RowArgs a) {
 #pragma unroll
         for (int it = 0; it < IT; ++it) sum += part[it];
       }
-      const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+      const Divisor root(root_of(sum, a));
       if constexpr (!kEarly) load_gamma();
+      if (root.near) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it)
+        for (int it = 0; it < IT; ++it)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[it][j] = v[it][j] * rstd * g[it][j];
+          for (int j = 0; j < 8; ++j) v[it][j] = root.fast(v[it][j]) * g[it][j];
+      } else {
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[it][j] = __fdiv_rn(v[it][j], root.d) * g[it][j];
+      }
     } else {
 #pragma unroll
       for (int it = 0; it < IT; ++it)
@@ -387,11 +413,12 @@ void launch_held(const RowArgs &a, hipStream_t st) {
   const bool vec = on16(a.x, a.ldx, xs) && on16(a.residual, a.ldr, xs) && on16(a.h, a.ldh, xs) &&
                    on16(a.y, a.ldy, a.y_bf16 ? 2 : 4) && on16(a.gamma, 0, 1) && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0;
   // The fewest registers that hold the row keep the most rows in flight; among the ways to
-  // split it the measured order (bf16, rows of 100 MB in all, us): 1024 wide: norm 47 at 1 x
+  // split it the measured order (bf16, 25 million elements, us): 1024 wide: norm 47 at 1 x
   // 2 (W x IT), SwiGLU 28, 47 and 32 at 2 x 1; 2048: norm 46 at 4 x 1, 47 at 2 x 2, SwiGLU 32
   // and 28; 4096: 49 and 28 at 4 x 2, 50 and 33 at 8 x 1; 6144: 51 and 36 at 12 x 1, 57 and
   // 31 at 4 x 3; 8192: 53 and 28 at 8 x 2, 59 and 35 at 16 x 1.  Of few rows the latency
-  // counts: one of 6144 takes 4.5 us at 12 x 1, 4.9 at 8 x 2, 5.3 at 4 x 3, 5.5 at 16 x 1.
+  // counts: one of 6144 takes 4.5 us at 12 x 1, 4.9 at 8 x 2, 5.3 at 4 x 3, 5.5 at 16 x 1
+  // (before the sums over lanes became fp64, which adds 0.2).
   constexpr bool norm = OP == kNorm;
   const bool few = a.S <= 64;
   if (a.H <= 512) launch_one<OP, BF16, 1, 1>(a, vec, st);

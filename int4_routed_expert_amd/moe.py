@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -74,7 +75,6 @@ def _load():
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     f32, f64 = ctypes.c_float, ctypes.c_double
     cp = ctypes.POINTER(moe_cfg)
-    rp = ctypes.POINTER(moe_rope_tensor)
     sigs = {
         "moe_validate_cfg": (ctypes.c_int, [cp]),
         "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -106,7 +106,7 @@ def _load():
         "moe_silu_quant": (ctypes.c_int, [p, p, i32, i64, i32, i32, p, i32, i64, p, i64, p, p]),
         "moe_qmatmul_workspace_bytes": (i64, [p, i64, p, i64, i32, i32, i32]),
         "moe_qmatmul": (ctypes.c_int, [p, i64, p, p, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
-        "moe_rope": (ctypes.c_int, [rp, rp, i32, i32, i32, i32, i32, i32, p, i32, p, f32, p]),
+        "moe_rope": (ctypes.c_int, [p, p, i32, i32, i32, i32, i32, i32, p, i32, p, f32, p]),
         "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f32)]),
         "moe_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_profile_report": (ctypes.c_int, [ctypes.c_char_p, sz]),
@@ -328,6 +328,7 @@ def moe_chain_destroy(chain: int | None) -> None:
 
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _ROWS = torch.contiguous_format
+_empty_like = torch.empty_like
 
 
 # ---- dense operators ---------------------------------------------------------------------------------------------------
@@ -381,6 +382,8 @@ def _code(dtype, what: str) -> int:
 def _rows(t, shape, what: str) -> int:
     """Row stride of the matrix t, whose rows must be contiguous and whose shape must be `shape`."""
     if t.shape == shape and len(shape) == 2:
+        if t.is_contiguous():
+            return shape[1]
         row, col = t.stride()
         if col == 1 or shape[1] <= 1:
             return row if shape[0] > 1 else shape[1]
@@ -389,13 +392,14 @@ def _rows(t, shape, what: str) -> int:
 
 
 def _vector(t, n: int, dtype, what: str) -> None:
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}, not {tuple(t.shape)} {t.dtype}")
 
 
 # The handle of a GPU's current stream.  Small calls are bound by this module's own time: the handle alone, where torch
 # has it, comes twenty times as fast as a stream object.
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _gpu(*tensors) -> int:
@@ -449,21 +453,21 @@ def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant:
     elif residual is None and not quant:
         raise ValueError("no output is asked for")
     gpu = _gpu(x, gamma, residual, h)
-    if stream is not None or gpu != torch.cuda.current_device():
+    if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, norm_quant, (x, gamma, residual, h), x, gamma, eps, residual, h, y_dtype, quant)
     y = q = d = None
     py = pq = pd = ph = pr = None
     if residual is not None:
         pr = residual.data_ptr()
         if h is None:
-            h = torch.empty_like(x, memory_format=_ROWS)
+            h = _empty_like(x, memory_format=_ROWS)
             ldh = H
         ph = h.data_ptr()
     if y_dtype is not None:
-        y = torch.empty_like(x, dtype=y_dtype, memory_format=_ROWS)
+        y = _empty_like(x, dtype=y_dtype, memory_format=_ROWS)
         py = y.data_ptr()
     if quant:
-        q, d = torch.empty_like(x, dtype=torch.int8, memory_format=_ROWS), x.new_empty(S, dtype=torch.float32)
+        q, d = _empty_like(x, dtype=torch.int8, memory_format=_ROWS), x.new_empty(S, dtype=torch.float32)
         pq, pd = q.data_ptr(), d.data_ptr()
     rc = _lib.moe_norm_quant(x.data_ptr(), xd, ldx, pr, ldr, gamma.data_ptr(), gd, eps, S, H, ph, ldh, py, yd, H, pq, H, pd,
                              _stream_of(gpu))
@@ -496,7 +500,7 @@ def silu_quant(g, u=None, y_dtype=None, quant: bool = True, stream=None):
     elif not quant:
         raise ValueError("no output is asked for")
     gpu = _gpu(g, u)
-    if stream is not None or gpu != torch.cuda.current_device():
+    if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, silu_quant, (g, u), g, u, y_dtype, quant)
     y = q = d = py = pq = pd = None
     if y_dtype is not None:
@@ -527,7 +531,7 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
     _vector(d, S, torch.float32, "d")
     _vector(dw, N, torch.float32, "dw")
     gpu = _gpu(q, d, w, dw, ws)
-    if stream is not None or gpu != torch.cuda.current_device():
+    if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, qmatmul, (q, d, w, dw, ws), q, d, w, dw, out_dtype, ws)
     pq, pw = q.data_ptr(), w.data_ptr()
     # operands on 16-byte boundaries take no workspace
@@ -544,6 +548,8 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
     return y
 
 
+_ROPE_TENSOR = struct.Struct("@PPqqqqi4x")  # moe_rope_tensor's bytes: packed, they cost a third of a ctypes structure
+assert _ROPE_TENSOR.size == ctypes.sizeof(moe_rope_tensor)
 _ROPE_SCALING = {"none": MOE_ROPE_PLAIN, "linear": MOE_ROPE_LINEAR, "ntk": MOE_ROPE_NTK, "yarn": MOE_ROPE_YARN}
 
 
@@ -583,17 +589,17 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
     half = freqs.shape[0] if freqs.dim() == 1 else -1
     _vector(freqs, half, torch.float64, "freqs")
     gpu = _gpu(q, k, pos, freqs)
-    if stream is not None or gpu != torch.cuda.current_device():
+    if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, rope, (q, k, pos, freqs), q, k, pos, freqs, offset, interleaved, factor, inplace)
     outs, args = [q, k], [None, None]
     for i, t in enumerate((q, k)):
         if t is None:
             continue
-        o = outs[i] = t if inplace else torch.empty_like(t, memory_format=_ROWS)
+        o = outs[i] = t if inplace else _empty_like(t, memory_format=_ROWS)
         s0, s1, _ = strides[i]
         heads = t.shape[1]
         o0, o1 = (s0, s1) if inplace else (heads * D, D)
-        args[i] = ctypes.byref(moe_rope_tensor(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, heads))
+        args[i] = _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, heads)
     rc = _lib.moe_rope(args[0], args[1], xd, S, D, 2 * half, offset,
                        MOE_ROPE_INTERLEAVED if interleaved else MOE_ROPE_HALF, pos.data_ptr(), wide, freqs.data_ptr(), factor,
                        _stream_of(gpu))
