@@ -287,11 +287,16 @@ __device__ inline __attribute__((always_inline)) void load_to_lds(const int8_t *
   asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p), "i"(off) : "memory", "scc");
 }
 
-// Waits until at most N of this wave's loads are in flight and its reads of LDS are done.
+// Waits until at most N of this wave's loads are in flight and its reads of LDS are done,
+// then for the workgroup's other waves.  One piece of assembly, so that no access to LDS
+// moves between the two.
 template <int N>
-__device__ inline void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+__device__ inline void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+
+// This wave's writes to LDS are done and seen by its reads.
+__device__ inline void own_lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 template <int BN, int BS, int WN, int WS, int NBUF, int KS>
 __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int tiles_n, int tiles_s, int group) {
@@ -396,8 +401,7 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
 #pragma unroll
     for (int i = 0; i < (s < NBUF - 1 ? kPer : kPer / kSpread); ++i) request(i, s);
   }
-  wait_loads<(NBUF - 2) * kPer + kPer / kSpread>();
-  __builtin_amdgcn_s_barrier();
+  wait_and_meet<(NBUF - 2) * kPer + kPer / kSpread>();
   i32x4 F[2][kG][kF];
 #pragma unroll
   for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
@@ -424,8 +428,7 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
     for (int g = 1; g < kGroups; ++g) {
       multiply((cur + g - 1) & 1, b, g, (b + NBUF - 1) % NBUF, g < kSpread ? kPer * g / kSpread : 0, g < kSpread ? kPer * (g + 1) / kSpread : 0);
     }
-    wait_loads<(NBUF - 2) * kPer>();
-    __builtin_amdgcn_s_barrier();
+    wait_and_meet<(NBUF - 2) * kPer>();
     clip(s + NBUF);
     multiply((cur + kGroups - 1) & 1, (b + 1) % NBUF, 0, b, 0, kPer / kSpread);
   };
@@ -437,9 +440,7 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
 #pragma unroll
   for (int b = 0; b < NBUF - 1; ++b)
     if (s + b < stages) stage(s + b, b);
-  wait_loads<0>();
-
-  __syncthreads();
+  wait_and_meet<0>();  // the last requests, beyond K, have arrived too
   if constexpr (KS > 1) {  // the first team adds the others' sums to its own
     i32x4 *sums = (i32x4 *)s_all;
     constexpr int kAcc = TN * TS * 4;  // pieces of four of a lane
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
       for (int e = 0; e < 4; ++e)
         *(i32x4 *)(out + row * kLd + i * 32 + 8 * e + 4 * ck) =
             i32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-    __builtin_amdgcn_wave_barrier();
+    own_lds_done();
     const int nl = wn * kWide + (lane % kRun) * 4;
     const float4 dw = *(const float4 *)(s_sc + nl);
 #pragma unroll 4
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
         store4(a, s0 + sl, n0 + nl, (float)v[0] * (ds * dw.x), (float)v[1] * (ds * dw.y), (float)v[2] * (ds * dw.z),
                (float)v[3] * (ds * dw.w));
     }
-    __builtin_amdgcn_wave_barrier();
+    own_lds_done();
   }
 }
 

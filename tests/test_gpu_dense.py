@@ -566,3 +566,32 @@ def test_example_layer(M, S):
     for got, want in ((got_h, want_h), (got_y, want_y)):
         assert (got.double() - want).norm() <= 0.05 * want.norm()
     assert moe.shape == (S, layer.c.hidden) and torch.isfinite(moe).all()
+
+
+def test_more_rows_than_one_launch(M):
+    """Numbers of rows, weights and tokens beyond what one launch or one pass of its workgroups takes."""
+    g = rng(5)
+    for S, H in (((1 << 22) + 9, 8), ((1 << 20) + 5, 520)):  # four rows and one row a workgroup
+        x = torch.randn(S, H, generator=g, device="cuda").bfloat16()
+        gamma = torch.rand(H, generator=g, device="cuda")
+        _, y, q, d = M.norm_quant(x, gamma, 1e-5, y_dtype=BF)
+        at = torch.tensor([0, 1, S // 2, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, S - 2, S - 1], device="cuda")
+        want = M.norm_quant(x[at], gamma, 1e-5, y_dtype=BF)
+        assert all(torch.equal(a[at], b) for a, b in zip((y, q, d), want[1:]))
+        z, zq, zd = M.silu_quant(x, x, y_dtype=BF)
+        assert all(torch.equal(a[at], b) for a, b in zip((z, zq, zd), M.silu_quant(x[at], x[at], y_dtype=BF)))
+        del x, y, q, z, zq
+    many = (1 << 18) + 7
+    for S, N, K in ((many, 5, 16), (3, many, 16), (many, 3, 13), (70, many, 33)):
+        q, d, w, dw = operands(g, S, N, K)
+        y = M.qmatmul(q, d, w, dw, out_dtype=F32)
+        want = (q.double() @ w.double().t().contiguous()).round().float() * (d[:, None] * dw)
+        assert torch.equal(y, want)
+        del y, want
+    S = (1 << 20) + 3
+    x = torch.randn(1, 2, 1024, generator=g, device="cuda").bfloat16().expand(S, 2, 1024)
+    pos = torch.randint(0, 5000, (S,), generator=g, device="cuda")
+    freqs, _ = M.rope_freqs(1024)
+    y, _ = M.rope(x, None, pos, freqs)
+    at = torch.tensor([0, 5, 1 << 19, (1 << 20) - 1, 1 << 20, S - 1], device="cuda")
+    assert torch.equal(y[at], M.rope(x[at], None, pos[at], freqs)[0])
