@@ -12,6 +12,7 @@
 //                                 operands zero: 484 us)
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "dense.h"
 
@@ -60,16 +61,23 @@ __device__ inline i32x4 load16_tail(const int8_t *row, int k, int K) {
   return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
-// Four neighbouring outputs y[s, n .. n + 3], those below N.
+// Four neighbouring outputs y[s, n .. n + 3], those below N, past the caches where STREAM.
+template <bool STREAM>
 __device__ inline void store4(const QmmArgs &a, int64_t s, int n, float v0, float v1, float v2, float v3) {
   const float v[4] = {v0, v1, v2, v3};
   if (a.y_vec && n + 4 <= a.N) {
     if (a.y_bf16) {
       const uint2 p = make_uint2((uint32_t)f_bf16(v0) | ((uint32_t)f_bf16(v1) << 16),
                                  (uint32_t)f_bf16(v2) | ((uint32_t)f_bf16(v3) << 16));
-      *(__attribute__((address_space(1))) uint64_t *)((uint16_t *)a.y + s * a.ldy + n) = ((uint64_t)p.y << 32) | p.x;
+      auto *to = (__attribute__((address_space(1))) uint64_t *)((uint16_t *)a.y + s * a.ldy + n);
+      const uint64_t both = ((uint64_t)p.y << 32) | p.x;
+      if constexpr (STREAM) __builtin_nontemporal_store(both, to);
+      else *to = both;
     } else {
-      stg<float4>((float *)a.y + s * a.ldy + n, make_float4(v0, v1, v2, v3));
+      auto *to = (__attribute__((address_space(1))) f32x4_t *)((float *)a.y + s * a.ldy + n);
+      const f32x4_t p = {v0, v1, v2, v3};
+      if constexpr (STREAM) __builtin_nontemporal_store(p, to);
+      else *to = p;
     }
   } else {
 #pragma unroll
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(64 * W) void k_qmm_few(QmmArgs a) {
       float v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = (float)sum[j] * (ds * ldg<float>(a.dw + min(n + j, a.N - 1)));
-      store4(a, s, n, v[0], v[1], v[2], v[3]);
+      store4<false>(a, s, n, v[0], v[1], v[2], v[3]);
     }
   }
 }
@@ -485,15 +493,19 @@ __global__ __launch_bounds__(64 * WN * WS * KS) void k_qmm_tile(QmmArgs a, int t
     own_lds_done();
     const int nl = wn * kWide + (lane % kRun) * 4;
     const float4 dw = *(const float4 *)(s_sc + nl);
+    auto leave = [&](auto stream) __attribute__((always_inline)) {
 #pragma unroll 4
-    for (int r = lane / kRun; r < 32; r += kTok) {
-      const int sl = wsv * (BS / WS) + j * 32 + r;
-      const i32x4 v = *(const i32x4 *)(out + r * kLd + (lane % kRun) * 4);
-      const float ds = s_sc[BN + sl];
-      if (s0 + sl < a.S && n0 + nl < a.N)
-        store4(a, s0 + sl, n0 + nl, (float)v[0] * (ds * dw.x), (float)v[1] * (ds * dw.y), (float)v[2] * (ds * dw.z),
-               (float)v[3] * (ds * dw.w));
-    }
+      for (int r = lane / kRun; r < 32; r += kTok) {
+        const int sl = wsv * (BS / WS) + j * 32 + r;
+        const i32x4 v = *(const i32x4 *)(out + r * kLd + (lane % kRun) * 4);
+        const float ds = s_sc[BN + sl];
+        if (s0 + sl < a.S && n0 + nl < a.N)
+          store4<decltype(stream)::value>(a, s0 + sl, n0 + nl, (float)v[0] * (ds * dw.x), (float)v[1] * (ds * dw.y),
+                                          (float)v[2] * (ds * dw.z), (float)v[3] * (ds * dw.w));
+      }
+    };
+    if (a.stream) leave(std::true_type());
+    else leave(std::false_type());
     own_lds_done();
   }
 }
@@ -643,6 +655,7 @@ void launch_piece(const QmmArgs &a, QmmKernel kernel, hipStream_t st) {
 hipError_t launch_qmatmul(const QmmArgs &a0, hipStream_t st) {
   QmmArgs a = a0;
   a.y_vec = (uintptr_t)a.y % (a.y_bf16 ? 8 : 16) == 0 && a.ldy % 4 == 0;
+  a.stream = (int64_t)a.S * a.N * (a.y_bf16 ? 2 : 4) > kStreamBytes;
   const QmmPlan p = plan_of(a);
   if (p.copy_q || p.copy_w) {
     ProfScope ps("qmatmul_align", st);

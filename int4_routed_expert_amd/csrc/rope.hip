@@ -62,18 +62,19 @@ __device__ inline void load_v(const void *p, int64_t i, float *v) {
   }
 }
 template <bool BF16, int V>
-__device__ inline void store_v(void *p, int64_t i, const float *v) {
+__device__ inline void store_v(void *p, int64_t i, const float *v, bool stream) {
   if constexpr (V == 1) {
     store_el<BF16>(p, i, v[0]);
   } else if constexpr (BF16 && V == 2) {
     stg<uint32_t>((uint16_t *)p + i, pack2_bf16(v[0], v[1]));
   } else if constexpr (BF16) {
-    stg<uint4>((uint16_t *)p + i, make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]),
-                                             pack2_bf16(v[6], v[7])));
+    const u32x4_t d = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
+    put((uint16_t *)p + i, d, stream);
   } else if constexpr (V == 2) {
     *(__attribute__((address_space(1))) f32x2_w *)((float *)p + i) = f32x2_w{v[0], v[1]};
   } else {
-    *(__attribute__((address_space(1))) f32x4_w *)((float *)p + i) = f32x4_w{v[0], v[1], v[2], v[3]};
+    const f32x4_t d = {v[0], v[1], v[2], v[3]};
+    put<4>((float *)p + i, d, stream);
   }
 }
 
@@ -89,8 +90,8 @@ struct RopePlan {
   uint32_t m_units, m_token;
 };
 
-// A turning unit: V pairs (half layout: V elements of each half; interleaved: V elements
-// from each of two neighbouring runs, or one pair where V = 1).  A copied unit: V elements.
+// A turning unit: V elements that form V / 2 neighbouring pairs (interleaved), or V pairs of
+// V elements of each half; one pair where V = 1.  A copied unit: V elements.
 template <bool BF16, int V, bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, RopePlan p) {
   __shared__ float2 s_cs[kRopeAngles];
@@ -123,33 +124,32 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, RopePlan p) {
       if (c >= a.offset) c += 2 * a.half;
       float v[V];
       load_v<BF16, V>(x, in + c, v);
-      store_v<BF16, V>(out, to + c, v);
+      store_v<BF16, V>(out, to + c, v, a.stream);
       continue;
     }
-    const int i0 = e * V;  // the unit's first pair
-    const int c1 = a.offset + (INTER ? 2 * i0 : i0), c2 = INTER ? c1 + V : c1 + a.half;
-    float v1[V], v2[V], w1[V], w2[V];
-    load_v<BF16, V>(x, in + c1, v1);
-    load_v<BF16, V>(x, in + c2, v2);
-    const float2 *cs = s_cs + t * a.half + i0;
+    // the fused operations are written out, so that every unit size gives the same bits
+    auto turn = [](float2 k, float x1, float x2, float &y1, float &y2) {
+      y1 = fmaf(x1, k.x, -(x2 * k.y));
+      y2 = fmaf(x2, k.x, x1 * k.y);
+    };
+    if constexpr (INTER && V > 1) {
+      float v[V], w[V];
+      load_v<BF16, V>(x, in + a.offset + e * V, v);
+      const float2 *cs = s_cs + t * a.half + e * (V / 2);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float2 k = cs[j];
-      // pair j's elements: half layout v1[j], v2[j]; interleaved elements 2j and 2j + 1 of v1 v2
-      const float x1 = INTER && V > 1 ? (2 * j < V ? v1[(2 * j) % V] : v2[(2 * j) % V]) : v1[j];
-      const float x2 = INTER && V > 1 ? (2 * j < V ? v1[(2 * j + 1) % V] : v2[(2 * j + 1) % V]) : v2[j];
-      // written as fused operations, so that both unit sizes give the same bits
-      const float y1 = fmaf(x1, k.x, -(x2 * k.y)), y2 = fmaf(x2, k.x, x1 * k.y);
-      if (INTER && V > 1) {
-        if (2 * j < V) { w1[(2 * j) % V] = y1; w1[(2 * j + 1) % V] = y2; }
-        else { w2[(2 * j) % V] = y1; w2[(2 * j + 1) % V] = y2; }
-      } else {
-        w1[j] = y1;
-        w2[j] = y2;
-      }
+      for (int j = 0; j < V / 2; ++j) turn(cs[j], v[2 * j], v[2 * j + 1], w[2 * j], w[2 * j + 1]);
+      store_v<BF16, V>(out, to + a.offset + e * V, w, a.stream);
+    } else {
+      const int c1 = a.offset + (INTER ? 2 * e : e * V), c2 = INTER ? c1 + 1 : c1 + a.half;
+      float v1[V], v2[V], w1[V], w2[V];
+      load_v<BF16, V>(x, in + c1, v1);
+      load_v<BF16, V>(x, in + c2, v2);
+      const float2 *cs = s_cs + t * a.half + e * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) turn(cs[j], v1[j], v2[j], w1[j], w2[j]);
+      store_v<BF16, V>(out, to + c1, w1, a.stream);
+      store_v<BF16, V>(out, to + c2, w2, a.stream);
     }
-    store_v<BF16, V>(out, to + c1, w1);
-    store_v<BF16, V>(out, to + c2, w2);
   }
 }
 
@@ -159,7 +159,7 @@ void launch(const RopeArgs &a, hipStream_t st) {
   // needs every row at a multiple of it.
   constexpr int kV = BF16 ? 8 : 4;
   auto fits = [&](int v) {
-    bool ok = a.D % v == 0 && a.offset % v == 0 && a.half % v == 0;
+    bool ok = a.D % v == 0 && a.offset % v == 0 && (INTER && v > 1 ? 2 * a.half : a.half) % v == 0;
     if (BF16)
       for (const auto &t : a.t)
         if (t.heads)
@@ -169,7 +169,7 @@ void launch(const RopeArgs &a, hipStream_t st) {
   };
   const int V = fits(kV) ? kV : fits(2) ? 2 : 1;
   RopePlan p{};
-  p.turning = a.half / V;
+  p.turning = INTER && V > 1 ? 2 * a.half / V : a.half / V;
   p.units = p.turning + (a.D - 2 * a.half) / V;
   const int per_token = (a.t[0].heads + a.t[1].heads) * p.units;
   // Tokens until a workgroup's threads all have a unit, while the angles fit and every
@@ -187,6 +187,7 @@ void launch(const RopeArgs &a, hipStream_t st) {
   const int64_t most = (int64_t)(1 << 20);
   for (int64_t at = 0; at < blocks; at += most) {
     RopeArgs c = a;
+    c.stream = (int64_t)a.S * (a.t[0].heads + a.t[1].heads) * a.D * (BF16 ? 2 : 4) > kStreamBytes;
     const int64_t s = at / p.parts * p.tokens;
     c.S = (int)(a.S - s);
     c.pos = (const char *)a.pos + s * (a.pos_i64 ? 8 : 4);

@@ -179,16 +179,26 @@ __device__ inline void load8(const void *p, int64_t i, float *v) {
   }
 }
 template <bool BF16, bool ON16>
-__device__ inline void store8(void *p, int64_t i, const float *v) {
+__device__ inline void store8(void *p, int64_t i, const float *v, bool stream) {
   if constexpr (BF16) {
     const u32x4_t d = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
     uint16_t *q = (uint16_t *)p + i;
-    if constexpr (ON16) *(__attribute__((address_space(1))) u32x4_t *)q = d;
+    if constexpr (ON16) put(q, d, stream);
     else *(__attribute__((address_space(1))) u32x4_h *)q = d;
   } else {
     float *q = (float *)p + i;
-    *(__attribute__((address_space(1))) f32x4_w *)q = f32x4_t{v[0], v[1], v[2], v[3]};
-    *(__attribute__((address_space(1))) f32x4_w *)(q + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    // both halves of a piece of 32 bytes together: past the caches, half lines cost a write each
+    auto *to = (__attribute__((address_space(1))) f32x4_w *)q;
+    if (stream) {
+      asm volatile("");
+      __builtin_nontemporal_store(a, to);
+      __builtin_nontemporal_store(b, (__attribute__((address_space(1))) f32x4_w *)(q + 4));
+      asm volatile("");
+    } else {
+      *to = a;
+      *(__attribute__((address_space(1))) f32x4_w *)(q + 4) = b;
+    }
   }
 }
 
@@ -205,10 +215,10 @@ __device__ inline void load_it(const void *p, int64_t row, int H, int tid, int i
   }
 }
 template <int W, bool ON16, bool BF16>
-__device__ inline void store_it(void *p, int64_t row, int H, int tid, int it, const float *v) {
+__device__ inline void store_it(void *p, int64_t row, int H, int tid, int it, const float *v, bool stream) {
   const int c = col_of<W>(tid, it);
   if (c + 8 <= H) {
-    store8<BF16, ON16>(p, row + c, v);
+    store8<BF16, ON16>(p, row + c, v, stream);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -318,7 +328,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : 1) v
           eight = fmaf(v[it][j], v[it][j], eight);
         }
         part[it] = wave_sum((double)eight);
-        if (a.h) store_it<W, ON16, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it]);
+        if (a.h) store_it<W, ON16, BF16>(a.h, r * a.ldh, a.H, tid, it, v[it], a.stream);
       }
       double sum = 0.;
       if constexpr (W > 1) {
@@ -355,8 +365,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : 1) v
     if (a.y) {
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        if (a.y_bf16) store_it<W, ON16, true>(a.y, r * a.ldy, a.H, tid, it, v[it]);
-        else store_it<W, ON16, false>(a.y, r * a.ldy, a.H, tid, it, v[it]);
+        if (a.y_bf16) store_it<W, ON16, true>(a.y, r * a.ldy, a.H, tid, it, v[it], a.stream);
+        else store_it<W, ON16, false>(a.y, r * a.ldy, a.H, tid, it, v[it], a.stream);
       }
     }
     if (a.q) {
@@ -384,7 +394,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : 1) v
         int8_t *to = a.q + r * a.ldq + k;
         if (k + 8 <= a.H) {
           const uint64_t both = ((uint64_t)w[1] << 32) | w[0];
-          if constexpr (ON16) *(__attribute__((address_space(1))) uint64_t *)to = both;
+          if constexpr (ON16) put(to, both, a.stream);
           else *(__attribute__((address_space(1))) u64_b *)to = both;
         } else {
 #pragma unroll
@@ -408,7 +418,10 @@ void launch_one(const RowArgs &a, bool vec, hipStream_t st) {
 bool on16(const void *p, int64_t ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }
 
 template <RowOp OP, bool BF16>
-void launch_held(const RowArgs &a, hipStream_t st) {
+void launch_held(const RowArgs &a0, hipStream_t st) {
+  RowArgs a = a0;
+  const int64_t each = (a.h ? (BF16 ? 2 : 4) : 0) + (a.y ? (a.y_bf16 ? 2 : 4) : 0) + (a.q ? 1 : 0);
+  a.stream = each * a.S * a.H > kStreamBytes;
   const int xs = BF16 ? 2 : 4;
   const bool vec = on16(a.x, a.ldx, xs) && on16(a.residual, a.ldr, xs) && on16(a.h, a.ldh, xs) &&
                    on16(a.y, a.ldy, a.y_bf16 ? 2 : 4) && on16(a.gamma, 0, 1) && (uintptr_t)a.q % 8 == 0 && a.ldq % 8 == 0;
