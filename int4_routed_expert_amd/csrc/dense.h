@@ -8,9 +8,11 @@
 namespace moe {
 
 // norm: x, residual, gamma, h; SwiGLU: x is the gate, residual the up rows.
-// Outputs of more than this go past the caches (non-temporal stores): the norm of 512 rows
-// of 6144 then takes 8.5 us in place of 10.2, of 2048 24 in place of 30, and the calls after
-// it are no slower; of 256 rows (8 MB) the product after it would be 2 us slower.
+// Outputs of more than this go past the caches (non-temporal stores), int8 rows aside: the
+// next call reads those, and reads them several times.  Norm of 512 rows of 6144 bf16: 8.9
+// us in place of 10.2, of 2048 24.7 in place of 29.5; norm, product and SwiGLU of 8192
+// tokens, one after another, 657 in place of 680 (675 with the int8 rows past the caches
+// too).  Of 256 rows (8 MB) the calls after the norm would be 2 us slower.
 constexpr int64_t kStreamBytes = 12 << 20;
 
 // A store of v at p (ALIGN: what p is surely aligned to), past the caches where `stream`.

@@ -6,10 +6,10 @@
 //                                 copy of 1 GiB runs at 5.1): bound by the weights' bytes
 //   256 x 6144 x 6144             18 us, 1.07 POP/s: a compute unit takes in about 80 KB/us
 //                                 past its XCD's L2, and the tiles move 1.2 MB through each
-//   8192 x 12288 x 6144           546 us, 2.27 POP/s (a library int8 product: 2.04): the
-//                                 matrix cores are busy 61% of the cycles, and the chip
-//                                 clocks down to 1.8 GHz to stay within its power (all
-//                                 operands zero: 484 us)
+//   8192 x 12288 x 6144           510 to 545 us on different cards, 2.27 to 2.43 POP/s (a
+//                                 library int8 product: 2.04): the matrix cores are busy
+//                                 61% of the cycles, and the chip clocks down to 1.8 GHz to
+//                                 stay within its power (all operands zero: 484 us)
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

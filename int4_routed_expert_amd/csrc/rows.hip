@@ -4,10 +4,10 @@
 //   then d = max|v| / 127 and q = rint(v / d).
 // Bound by memory: the row stays in registers between the statistics and the outputs, so
 // each input is read and each output written once (counters: 1.00 times the unique bytes).
-// Measured: norm 8192 x 6144 bf16 with residual, norm and int8 rows 99 us, 4.6 TB/s (fp32
-// in: 132 us, 5.7); SwiGLU 4096 x 12288 bf16 65 us, 3.9 TB/s (fp32: 85 us, 5.3; a copy of 1
+// Measured: norm 8192 x 6144 bf16 with residual, norm and int8 rows 97 us, 4.7 TB/s (fp32
+// in: 132 us, 5.7); SwiGLU 4096 x 12288 bf16 63 us, 4.0 TB/s (fp32: 85 us, 5.3; a copy of 1
 // GiB runs at 5.1): in bf16 the exponential and the divisions take about as long as the
-// memory.  One row of 6144: 4.8 us, two barriers and a trip to memory.
+// memory.  One row of 6144: 4.7 us, two barriers and a trip to memory.
 #include <algorithm>
 
 #include "dense.h"
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : 1) v
         int8_t *to = a.q + r * a.ldq + k;
         if (k + 8 <= a.H) {
           const uint64_t both = ((uint64_t)w[1] << 32) | w[0];
-          if constexpr (ON16) put(to, both, a.stream);
+          if constexpr (ON16) *(__attribute__((address_space(1))) uint64_t *)to = both;
           else *(__attribute__((address_space(1))) u64_b *)to = both;
         } else {
 #pragma unroll
