@@ -1,6 +1,7 @@
 // Product of int8 rows with int8 weights: y[s, n] = (sum_k q[s, k] w[n, k]) * (d[s] * dw[n]),
 // the sum exact in int32, scaled once in fp32.  Three kernels, chosen by estimated time
-// (plan_of): a dot-product kernel for up to four tokens, a direct matrix-core kernel for
+// (plan_of): a dot-product kernel for up to four tokens (eight where weight rows are few), a
+// direct matrix-core kernel for
 // few tokens or small operands, LDS tiles for the others.  Measured (bf16 outputs):
 //   1 x 4096 x 6144 (S x N x K)   5.8 us, 4.3 TB/s; 1 x 12288 x 6144 12.4 us, 6.1 TB/s (a
 //                                 copy of 1 GiB runs at 5.1): bound by the weights' bytes
@@ -533,6 +534,8 @@ bool on16(const int8_t *p, int64_t ld, int rows, int K) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && K % 16 == 0;
 }
 
+constexpr int kVecFew = 1024;
+
 struct QmmPlan {
   QmmKernel kernel;
   bool copy_q, copy_w;  // rows that the tiles need on 16-byte boundaries first
@@ -546,7 +549,9 @@ struct QmmPlan {
 QmmPlan plan_of(const QmmArgs &a) {
   QmmPlan p{};
   const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);
-  if (a.S <= 4) {
+  // up to eight tokens and few rows of a long K too: 8 x 576 x 6144 4.0 us (the direct matrix
+  // kernel 6.2, by 36 workgroups), 8 x 1024 x 16384 8.4 (13.8)
+  if (a.S <= 4 || (a.S <= 8 && a.N <= kVecFew && a.K >= 2048)) {
     p.kernel = kVec;
     return p;
   }
@@ -593,12 +598,21 @@ void launch_vec(const QmmArgs &a, hipStream_t st) {
   MOE_LAUNCH((k_qmm_vec<NS, R, KS, W4>), dim3((unsigned)((a.N + rows - 1) / rows)), dim3(256), 0, st, a);
 }
 
+// Few rows of a long K: four waves share one (1 x 576 x 16384 2.8 us, 3.3 by one wave).  Two
+// rows a wave meet the same tokens where there are tokens to share and rows enough (4 x 4096
+// x 6144 6.4 us, 7.1 by one row; 1 x 2048 x 6144 4.1 and 3.7).
 template <int NS, bool W4>
 void launch_vec_for(const QmmArgs &a, hipStream_t st) {
-  // few rows: four waves share one; more: two rows a wave meet the same tokens
-  if (a.N <= 1024) launch_vec<NS, 1, 4, W4>(a, st);
-  else if (a.N <= 8192) launch_vec<NS, 1, 1, W4>(a, st);
-  else launch_vec<NS, 2, 1, W4>(a, st);
+  if constexpr (NS > 4) {
+    launch_vec<NS, 1, 4, W4>(a, st);
+  } else if (a.N <= kVecFew && a.K > 8192) {
+    launch_vec<NS, 1, 4, W4>(a, st);
+  } else {
+    if constexpr (NS > 1) {
+      if (a.N > 2048) return launch_vec<NS, 2, 1, W4>(a, st);
+    }
+    launch_vec<NS, 1, 1, W4>(a, st);
+  }
 }
 
 template <int NT, bool W4>
@@ -613,7 +627,8 @@ void launch_direct(const QmmArgs &a, QmmKernel k, hipStream_t st) {
   else if (k == kFew2) launch_few<2, W4>(a, st);
   else if (a.S == 1) launch_vec_for<1, W4>(a, st);
   else if (a.S == 2) launch_vec_for<2, W4>(a, st);
-  else launch_vec_for<4, W4>(a, st);
+  else if (a.S <= 4) launch_vec_for<4, W4>(a, st);
+  else launch_vec_for<8, W4>(a, st);
 }
 
 template <int BN, int BS, int WN, int WS, int NBUF, int KS>

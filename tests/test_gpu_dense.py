@@ -259,7 +259,8 @@ def test_product(M, S, N, K, pad, start):
 
 
 @pytest.mark.parametrize("S,N,K,kernel", [
-    (1, 500, 300, "vec"), (3, 20000, 64, "vec"), (4, 4000, 1040, "vec"), (9, 300, 1030, "few"), (64, 700, 512, "few"),
+    (1, 500, 300, "vec"), (3, 20000, 64, "vec"), (6, 576, 6144, "vec"), (8, 1000, 2064, "vec"), (5, 1024, 9008, "vec"),
+    (2, 900, 8208, "vec"), (4, 700, 16400, "vec"), (1, 600, 8256, "vec"), (2, 2500, 1040, "vec"), (8, 1000, 2049, "vec"), (4, 4000, 1040, "vec"), (9, 300, 1030, "few"), (64, 700, 512, "few"),
     (130, 700, 272, "few32"), (17, 4100, 272, "few32"), (17, 4096, 4112, "tile32"), (130, 1024, 2064, "tile32"),
     (30, 700, 16400, "tile32"), (260, 1024, 528, "tile32x64"), (1540, 300, 272, "tile32x64"),
     (770, 1024, 272, "tile64"), (48, 8208, 528, "tile64"), (200, 6160, 2064, "tile64x128"), (770, 4096, 272, "tile128"),
