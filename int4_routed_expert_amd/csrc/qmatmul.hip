@@ -1,8 +1,8 @@
 // Product of int8 rows with int8 weights: y[s, n] = (sum_k q[s, k] w[n, k]) * (d[s] * dw[n]),
 // the sum exact in int32, scaled once in fp32.  Three kernels, chosen by estimated time
-// (plan_of): a dot-product kernel for up to four tokens (eight where weight rows are few), a
-// direct matrix-core kernel for
-// few tokens or small operands, LDS tiles for the others.  Measured (bf16 outputs):
+// (plan_of): a dot-product kernel for up to four tokens (eight where weight rows are few and
+// long), a direct matrix-core kernel for few tokens or small operands, LDS tiles for the
+// others.  Measured (bf16 outputs):
 //   1 x 4096 x 6144 (S x N x K)   5.8 us, 4.3 TB/s; 1 x 12288 x 6144 12.4 us, 6.1 TB/s (a
 //                                 copy of 1 GiB runs at 5.1): bound by the weights' bytes
 //   256 x 6144 x 6144             18 us, 1.07 POP/s: a compute unit takes in about 80 KB/us
