@@ -549,8 +549,12 @@ struct QmmPlan {
 QmmPlan plan_of(const QmmArgs &a) {
   QmmPlan p{};
   const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);
-  // up to eight tokens and few rows of a long K too: 8 x 576 x 6144 4.0 us (the direct matrix
-  // kernel 6.2, by 36 workgroups), 8 x 1024 x 16384 8.4 (13.8)
+  // Up to four tokens by dot products, the direct matrix kernel's time in brackets: 1 x 576 x
+  // 6144 2.4 us (5.3), 1 x 4096 x 6144 5.8 (7.1), 4 x 4096 x 6144 6.4 (7.4), 4 x 12288 x 6144
+  // 13.2 (14.5); behind it only at four tokens of a short K (4 x 4096 x 512 2.9 (2.6)) or of
+  // very many rows (4 x 32768 x 6144 43 (41)).  Up to eight where rows are few and long:
+  // 8 x 576 x 6144 3.9 (6.2, by 36 workgroups), 8 x 1024 x 2048 3.5 (3.5), 8 x 1024 x 16384
+  // 8.4 (13.2).
   if (a.S <= 4 || (a.S <= 8 && a.N <= kVecFew && a.K >= 2048)) {
     p.kernel = kVec;
     return p;
