@@ -332,31 +332,44 @@ _empty_like = torch.empty_like
 
 
 # ---- dense operators ---------------------------------------------------------------------------------------------------
+# The ABI's sizes are int32, and ctypes would pass on the low 32 bits of a larger one.
+
+def _sizes(where: str, *sizes) -> None:
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise MoeError(MOE_EINVAL, where)
+
 
 def moe_norm_quant(x, x_dtype: int, ldx: int, residual, ldr: int, gamma, g_dtype: int, eps: float, S: int, H: int, h,
                    ldh: int, y, y_dtype: int, ldy: int, q, ldq: int, d, stream=None) -> None:
+    _sizes("moe_norm_quant", S, H)
     _check(_lib.moe_norm_quant(ptr(x), x_dtype, ldx, ptr(residual), ldr, ptr(gamma), g_dtype, eps, S, H, ptr(h), ldh,
                                ptr(y), y_dtype, ldy, ptr(q), ldq, ptr(d), stream_handle(stream)), "moe_norm_quant")
 
 
 def moe_silu_quant(g, u, x_dtype: int, ldx: int, S: int, I: int, y, y_dtype: int, ldy: int, q, ldq: int, d,
                    stream=None) -> None:
+    _sizes("moe_silu_quant", S, I)
     _check(_lib.moe_silu_quant(ptr(g), ptr(u), x_dtype, ldx, S, I, ptr(y), y_dtype, ldy, ptr(q), ldq, ptr(d),
                                stream_handle(stream)), "moe_silu_quant")
 
 
 def moe_qmatmul_workspace_bytes(q, ldq: int, w, ldw: int, S: int, N: int, K: int) -> int:
+    if max(S, N, K) > 0x7FFFFFFF or min(S, N, K) < 0:
+        return MOE_EINVAL
     return _lib.moe_qmatmul_workspace_bytes(ptr(q), ldq, ptr(w), ldw, S, N, K)
 
 
 def moe_qmatmul(q, ldq: int, d, w, ldw: int, dw, S: int, N: int, K: int, y, y_dtype: int, ldy: int, ws, ws_bytes: int,
                 stream=None) -> None:
+    _sizes("moe_qmatmul", S, N, K)
     _check(_lib.moe_qmatmul(ptr(q), ldq, ptr(d), ptr(w), ldw, ptr(dw), S, N, K, ptr(y), y_dtype, ldy, ptr(ws), ws_bytes,
                             stream_handle(stream)), "moe_qmatmul")
 
 
 def moe_rope(q: moe_rope_tensor, k: moe_rope_tensor | None, x_dtype: int, S: int, D: int, rot: int, offset: int,
              layout: int, pos, pos_i64: int, freqs, factor: float, stream=None) -> None:
+    _sizes("moe_rope", S, D, rot, offset)
     _check(_lib.moe_rope(ctypes.byref(q), None if k is None else ctypes.byref(k), x_dtype, S, D, rot, offset, layout,
                          ptr(pos), pos_i64, ptr(freqs), factor, stream_handle(stream)), "moe_rope")
 
@@ -365,6 +378,7 @@ def moe_rope_freqs(rot: int, theta: float, scaling: int, scale: float, trained_l
                    beta_slow: float):
     """(float64 numpy array [rot / 2], factor)."""
     import numpy as np
+    _sizes("moe_rope_freqs", rot, trained_length)
     out = np.empty(max(rot, 0) // 2, np.float64)
     factor = ctypes.c_float(0.0)
     _check(_lib.moe_rope_freqs(rot, theta, scaling, scale, trained_length, beta_fast, beta_slow, ptr(out),
@@ -452,6 +466,8 @@ def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant:
         yd = _code(y_dtype, "y_dtype")
     elif residual is None and not quant:
         raise ValueError("no output is asked for")
+    if (S | H) >> 31:
+        _sizes("moe_norm_quant", S, H)
     gpu = _gpu(x, gamma, residual, h)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, norm_quant, (x, gamma, residual, h), x, gamma, eps, residual, h, y_dtype, quant)
@@ -499,6 +515,8 @@ def silu_quant(g, u=None, y_dtype=None, quant: bool = True, stream=None):
         yd = _code(y_dtype, "y_dtype")
     elif not quant:
         raise ValueError("no output is asked for")
+    if (S | I) >> 31:
+        _sizes("moe_silu_quant", S, I)
     gpu = _gpu(g, u)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, silu_quant, (g, u), g, u, y_dtype, quant)
@@ -530,6 +548,8 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
         raise ValueError(f"q and w must be int8, not {q.dtype} and {w.dtype}")
     _vector(d, S, torch.float32, "d")
     _vector(dw, N, torch.float32, "dw")
+    if (S | N | K) >> 31:
+        _sizes("moe_qmatmul", S, N, K)
     gpu = _gpu(q, d, w, dw, ws)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, qmatmul, (q, d, w, dw, ws), q, d, w, dw, out_dtype, ws)
@@ -588,6 +608,7 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
     _vector(pos, S, pos.dtype, "pos")
     half = freqs.shape[0] if freqs.dim() == 1 else -1
     _vector(freqs, half, torch.float64, "freqs")
+    _sizes("moe_rope", S, D, 2 * half, offset, q.shape[1], 0 if k is None else k.shape[1])
     gpu = _gpu(q, k, pos, freqs)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, rope, (q, k, pos, freqs), q, k, pos, freqs, offset, interleaved, factor, inplace)

@@ -1,0 +1,71 @@
+"""Calls of the dense operators that have to be refused, or to leave a mark, before anything runs (no GPU needed)."""
+import pytest
+import torch
+
+from int4_routed_expert_amd import moe as M
+
+A = 1 << 20  # an address that is never read: every call here is refused
+BIG = [1 << 31, (1 << 32) + 2]  # the second one's low 32 bits are an ordinary size
+
+
+def wide(n, m, dtype=torch.float32):
+    """[n, m] of one element's memory along n, or along m where m is large (contiguous rows, which need real ones)."""
+    return torch.zeros((1, m), dtype=dtype).expand(n, m)
+
+
+def i8(*shape):
+    return torch.zeros(shape, dtype=torch.int8)
+
+
+@pytest.mark.parametrize("n", BIG)
+@pytest.mark.parametrize("call", [
+    lambda n: M.norm_quant(wide(n, 8), torch.zeros(8), 1e-5),
+    lambda n: M.silu_quant(wide(n, 8)),
+    lambda n: M.silu_quant(wide(n, 8), wide(n, 8)),
+    lambda n: M.qmatmul(wide(n, 16, torch.int8), torch.zeros(()).expand(n), i8(4, 16), torch.zeros(4)),
+    lambda n: M.qmatmul(i8(2, 16), torch.zeros(2), wide(n, 16, torch.int8), torch.zeros(()).expand(n)),
+    lambda n: M.rope(torch.zeros(1, 2, 8).expand(n, 2, 8), None, torch.zeros((), dtype=torch.int64).expand(n),
+                     torch.zeros(4, dtype=torch.float64)),
+    lambda n: M.rope(torch.zeros(2, 1, 8).expand(2, n, 8), None, torch.zeros(2, dtype=torch.int64),
+                     torch.zeros(4, dtype=torch.float64)),
+    lambda n: M.rope(torch.zeros(2, 1, 8), torch.zeros(2, 1, 8).expand(2, n, 8), torch.zeros(2, dtype=torch.int64),
+                     torch.zeros(4, dtype=torch.float64)),
+    lambda n: M.rope(torch.zeros(2, 1, 8), None, torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.float64),
+                     offset=n),
+    lambda n: M.rope_freqs(n, device="cpu"),
+    lambda n: M.rope_freqs(64, 10000.0, "yarn", 4.0, n, device="cpu"),
+    lambda n: M.moe_norm_quant(A, 0, 64, None, 0, A, 0, 1e-5, n, 64, None, 0, A, 0, 64, None, 0, None, 0),
+    lambda n: M.moe_norm_quant(A, 0, n, None, 0, A, 0, 1e-5, 1, n, None, 0, A, 0, n, None, 0, None, 0),
+    lambda n: M.moe_silu_quant(A, A, 0, 64, n, 64, A, 0, 64, None, 0, None, 0),
+    lambda n: M.moe_silu_quant(A, A, 0, n, 1, n, A, 0, n, None, 0, None, 0),
+    lambda n: M.moe_qmatmul(A, 64, A, A, 64, A, n, 4, 64, A, 0, 4, None, 0, 0),
+    lambda n: M.moe_qmatmul(A, 64, A, A, 64, A, 1, n, 64, A, 0, n, None, 0, 0),
+    lambda n: M.moe_qmatmul(A, n, A, A, n, A, 1, 4, n, A, 0, 4, None, 0, 0),
+    lambda n: M.moe_rope(M.moe_rope_tensor(A, A, 8, 8, 8, 8, 1), None, 0, n, 8, 8, 0, 0, A, 1, A, 1.0, 0),
+    lambda n: M.moe_rope(M.moe_rope_tensor(A, A, 8, 8, 8, 8, 1), None, 0, 1, n, 8, 0, 0, A, 1, A, 1.0, 0),
+    lambda n: M.moe_rope(M.moe_rope_tensor(A, A, 8, 8, 8, 8, 1), None, 0, 1, 8, n, 0, 0, A, 1, A, 1.0, 0),
+    lambda n: M.moe_rope(M.moe_rope_tensor(A, A, 8, 8, 8, 8, 1), None, 0, 1, 8, 2, n, 0, A, 1, A, 1.0, 0),
+])
+def test_sizes_beyond_the_abi(call, n, monkeypatch):
+    """Sizes that the ABI's 32 bits do not hold are refused as a size out of range, not cut to their low bits."""
+    def never(*args):
+        raise AssertionError("the C entry was called")
+    for name in ("moe_norm_quant", "moe_silu_quant", "moe_qmatmul", "moe_rope", "moe_rope_freqs"):
+        monkeypatch.setattr(M._lib, name, never)
+    monkeypatch.setattr(M, "_vector", lambda *args: None)  # the vectors of such sizes are stand-ins of one element
+    with pytest.raises(M.MoeError) as e:
+        call(n)
+    assert e.value.status == M.MOE_EINVAL
+
+
+@pytest.mark.parametrize("n", BIG)
+def test_workspace_of_sizes_beyond_the_abi(n):
+    for S, N, K in ((n, 4, 64), (4, n, 64), (4, 4, n)):
+        assert M.moe_qmatmul_workspace_bytes(A, 64, A, 64, S, N, K) == M.MOE_EINVAL
+
+
+@pytest.mark.parametrize("rot", [-2, -(1 << 31) + 2])
+def test_negative_sizes_reach_the_check(rot):
+    with pytest.raises(M.MoeError) as e:
+        M.rope_freqs(rot, device="cpu")
+    assert e.value.status == M.MOE_EINVAL
