@@ -548,6 +548,8 @@ def qmatmul(q, d, w, dw, out_dtype=None, ws=None, stream=None):
         raise ValueError(f"q and w must be int8, not {q.dtype} and {w.dtype}")
     _vector(d, S, torch.float32, "d")
     _vector(dw, N, torch.float32, "dw")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, not of strides {tuple(ws.stride())}")
     if (S | N | K) >> 31:
         _sizes("moe_qmatmul", S, N, K)
     gpu = _gpu(q, d, w, dw, ws)

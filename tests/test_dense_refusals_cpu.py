@@ -69,3 +69,10 @@ def test_negative_sizes_reach_the_check(rot):
     with pytest.raises(M.MoeError) as e:
         M.rope_freqs(rot, device="cpu")
     assert e.value.status == M.MOE_EINVAL
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2]])
+def test_workspace_has_to_be_one_piece(ws):
+    """A tensor whose elements do not lie one after another has less memory, or other memory, than its size says."""
+    with pytest.raises(ValueError, match="ws"):
+        M.qmatmul(i8(70, 33), torch.zeros(70), i8(9, 33), torch.zeros(9), ws=ws)
