@@ -18,6 +18,11 @@ int status(hipError_t e) {
   return MOE_EHIP;
 }
 
+// An output of S rows at the address of an input: it has to be that input's type and stride.
+bool in_place_ok(const void *out, int out_size, int64_t ldo, const void *in, int in_size, int64_t ldi, int32_t S) {
+  return !out || out != in || (out_size == in_size && (S == 1 || ldo == ldi));
+}
+
 // The outputs that norm and SwiGLU share.
 int check_rows(const RowArgs &a, int32_t y_dtype) {
   if ((a.q == nullptr) != (a.d == nullptr)) return MOE_ENULL;
@@ -44,6 +49,9 @@ int moe_norm_quant(const void *x, int32_t x_dtype, int64_t ldx, const void *resi
   if (ldx < 0 || !aligned(x, xs) || !aligned(gamma, size_of(g_dtype)) ||
       (residual && (ldr < 0 || !aligned(residual, xs))) || (h && (ldh < H || !aligned(h, xs))))
     return MOE_EINVAL;
+  if (!in_place_ok(h, xs, ldh, x, xs, ldx, S) || !in_place_ok(h, xs, ldh, residual, xs, ldr, S) ||
+      !in_place_ok(y, size_of(y_dtype), ldy, x, xs, ldx, S))
+    return MOE_EINVAL;
   RowArgs a{};
   a.S = S; a.H = H; a.eps = eps;
   a.g_bf16 = g_dtype == MOE_BF16; a.y_bf16 = y_dtype == MOE_BF16;
@@ -61,6 +69,8 @@ int moe_silu_quant(const void *g, const void *u, int32_t x_dtype, int64_t ldx, i
   if (!g || !u || (!y && !q && !d)) return MOE_ENULL;
   const int xs = size_of(x_dtype);
   if (ldx < 0 || !aligned(g, xs) || !aligned(u, xs)) return MOE_EINVAL;
+  if (!in_place_ok(y, size_of(y_dtype), ldy, g, xs, ldx, S) || !in_place_ok(y, size_of(y_dtype), ldy, u, xs, ldx, S))
+    return MOE_EINVAL;
   RowArgs a{};
   a.S = S; a.H = I; a.y_bf16 = y_dtype == MOE_BF16;
   a.x = g; a.residual = u; a.y = y; a.q = q; a.d = d;

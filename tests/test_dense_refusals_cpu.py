@@ -76,3 +76,24 @@ def test_workspace_has_to_be_one_piece(ws):
     """A tensor whose elements do not lie one after another has less memory, or other memory, than its size says."""
     with pytest.raises(ValueError, match="ws"):
         M.qmatmul(i8(70, 33), torch.zeros(70), i8(9, 33), torch.zeros(9), ws=ws)
+
+
+F, B = M.MOE_F32, M.MOE_BF16
+X, R, Y, Q = (A + (i << 24) for i in range(4))
+
+
+def norm(x=X, xd=B, ldx=64, res=None, ldr=0, h=None, ldh=0, y=None, yd=B, ldy=0, q=None, S=2):
+    return M._lib.moe_norm_quant(x, xd, ldx, res, ldr, A, F, 1e-5, S, 64, h, ldh, y, yd, ldy, q, 64, q, None)
+
+
+def silu(y, yd=B, ldy=64, ldx=64, S=2):
+    return M._lib.moe_silu_quant(X, R, B, ldx, S, 64, y, yd, ldy, None, 0, None, None)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: norm(y=X, yd=F, ldy=64), lambda: norm(xd=F, ldx=64, y=X, yd=B, ldy=64), lambda: norm(y=X, ldy=72),
+    lambda: norm(res=R, ldr=64, h=R, ldh=72), lambda: norm(res=R, ldr=64, h=X, ldh=72), lambda: norm(y=X, yd=F, ldy=64, S=1),
+    lambda: silu(X, yd=F), lambda: silu(R, yd=F), lambda: silu(X, ldy=72), lambda: silu(R, ldy=72, ldx=80)])
+def test_in_place_at_another_type_or_stride(call):
+    """An output over its input has to have its type and stride: rows would be written over rows not read yet."""
+    assert call() == M.MOE_EINVAL
