@@ -416,12 +416,21 @@ _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: 
 _current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+_recording = torch.is_grad_enabled
+
+
 def _gpu(*tensors) -> int:
-    """The index of the GPU that every given tensor is on."""
+    """The index of the GPU that every given tensor is on.  None may ask for gradients where torch records them: these
+    calls have no backward pass, and their outputs would be cut off from the graph without a word."""
     i = tensors[0].get_device()
+    recording = _recording()
     for t in tensors:
-        if t is not None and t.get_device() != i:
-            raise ValueError(f"the tensors must be on one GPU, not on {tensors[0].device} and {t.device}")
+        if t is not None:
+            if recording and t.requires_grad:
+                raise ValueError("this call has no backward pass: make it under torch.no_grad(), or detach the tensors that "
+                                 "require gradients")
+            if t.get_device() != i:
+                raise ValueError(f"the tensors must be on one GPU, not on {tensors[0].device} and {t.device}")
     if i < 0:
         raise ValueError(f"the tensors must be on a GPU, not on {tensors[0].device}")
     return i

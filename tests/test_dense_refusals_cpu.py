@@ -97,3 +97,31 @@ def silu(y, yd=B, ldy=64, ldx=64, S=2):
 def test_in_place_at_another_type_or_stride(call):
     """An output over its input has to have its type and stride: rows would be written over rows not read yet."""
     assert call() == M.MOE_EINVAL
+
+
+def grad(*shape):
+    return torch.zeros(shape, requires_grad=True)
+
+
+POS, FREQS = torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=torch.float64)
+WITH_GRAD = [
+    lambda: M.norm_quant(grad(2, 8), torch.zeros(8), 1e-5),
+    lambda: M.norm_quant(torch.zeros(2, 8), grad(8), 1e-5),
+    lambda: M.norm_quant(torch.zeros(2, 8), torch.zeros(8), 1e-5, residual=grad(2, 8)),
+    lambda: M.silu_quant(grad(2, 8)),
+    lambda: M.silu_quant(torch.zeros(2, 8), grad(2, 8)),
+    lambda: M.qmatmul(i8(2, 8), grad(2), i8(4, 8), torch.zeros(4)),
+    lambda: M.qmatmul(i8(2, 8), torch.zeros(2), i8(4, 8), grad(4)),
+    lambda: M.rope(grad(2, 4, 8), None, POS, FREQS),
+    lambda: M.rope(torch.zeros(2, 4, 8), grad(2, 1, 8), POS, FREQS),
+]
+
+
+@pytest.mark.parametrize("call", WITH_GRAD)
+def test_no_gradient_is_lost_silently(call):
+    """There is no backward pass: an input that asks for gradients is refused where torch would record the call."""
+    with pytest.raises(ValueError, match="no_grad"):
+        call()
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off, pytest.raises(ValueError, match="on a GPU"):  # past that check, refused for the CPU tensors
+            call()
