@@ -417,6 +417,7 @@ _current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_
 
 
 _recording = torch.is_grad_enabled
+_written = torch.autograd.graph.increment_version  # of a tensor that a call wrote over
 
 
 def _gpu(*tensors) -> int:
@@ -482,6 +483,7 @@ def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant:
         return _elsewhere(gpu, stream, norm_quant, (x, gamma, residual, h), x, gamma, eps, residual, h, y_dtype, quant)
     y = q = d = None
     py = pq = pd = ph = pr = None
+    over = h
     if residual is not None:
         pr = residual.data_ptr()
         if h is None:
@@ -498,6 +500,8 @@ def norm_quant(x, gamma, eps: float, residual=None, h=None, y_dtype=None, quant:
                              _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_norm_quant")
+    if over is not None:
+        _written(over)
     return h, y, q, d
 
 
@@ -637,6 +641,10 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
                        _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_rope")
+    if inplace:
+        _written(q)
+        if k is not None:
+            _written(k)
     return outs[0], outs[1]
 
 

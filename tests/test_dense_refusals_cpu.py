@@ -125,3 +125,43 @@ def test_no_gradient_is_lost_silently(call):
     for off in (torch.no_grad(), torch.inference_mode()):
         with off, pytest.raises(ValueError, match="on a GPU"):  # past that check, refused for the CPU tensors
             call()
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The binding's calls on CPU tensors, up to the C entries, which do nothing."""
+    monkeypatch.setattr(M, "_gpu", lambda *tensors: 0)
+    monkeypatch.setattr(M, "_current_gpu", lambda: 0)
+    monkeypatch.setattr(M, "_stream_of", lambda gpu: None)
+    for name in ("moe_norm_quant", "moe_rope"):
+        monkeypatch.setattr(M._lib, name, lambda *args: 0)
+
+
+def test_in_place_writes_raise_the_version(on_cpu):
+    """A tensor that a call writes over counts as changed, so that torch refuses a backward pass through its old values."""
+    x, r, g = torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(8)
+    versions = lambda *ts: [t._version for t in ts]  # noqa: E731
+    before = versions(x, r, g)
+    h = M.norm_quant(x, g, 1e-5, residual=r, h=r)[0]
+    assert h is r and versions(x, r, g) == [before[0], before[1] + 1, before[2]]
+    M.norm_quant(x, g, 1e-5, residual=r, h=x)
+    assert versions(x, r) == [before[0] + 1, before[1] + 1]
+    M.norm_quant(x, g, 1e-5, residual=r)
+    assert versions(x, r) == [before[0] + 1, before[1] + 1]
+    both = torch.zeros(2, 5, 8)
+    q, k = both[:, :4], both[:, 4:]
+    M.rope(q, k, POS, FREQS)
+    assert both._version == 0
+    M.rope(q, k, POS, FREQS, inplace=True)
+    assert both._version > 0
+    k = torch.zeros(2, 1, 8)
+    M.rope(torch.zeros(2, 4, 8), k, POS, FREQS, inplace=True)
+    assert k._version == 1
+    leaf = torch.ones(2, 8, requires_grad=True)
+    saved = torch.ones(2, 8)
+    loss = (leaf * saved).sum()
+    M.norm_quant(x, g, 1e-5, residual=saved, h=saved)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        M.norm_quant(torch.zeros(2, 8), g, 1e-5, residual=r, h=torch.zeros(2, 8))
