@@ -440,6 +440,8 @@ def _gpu(*tensors) -> int:
 def _elsewhere(gpu: int, stream, f, inputs, *args, **kw):
     """f(*args, **kw) with `gpu`, and `stream` where one is given, made current: the outputs that f allocates then belong
     to the stream that writes them, and the memory of its inputs is not given out again before that stream is done."""
+    if getattr(stream, "device_index", gpu) != gpu:
+        raise ValueError(f"the stream is one of GPU {stream.device_index}, the tensors are on GPU {gpu}")
     with torch.cuda.device(gpu):
         if stream is None:
             return f(*args, **kw)

@@ -165,3 +165,13 @@ def test_in_place_writes_raise_the_version(on_cpu):
         loss.backward()
     with torch.inference_mode():
         M.norm_quant(torch.zeros(2, 8), g, 1e-5, residual=r, h=torch.zeros(2, 8))
+
+
+class OtherGpusStream:
+    cuda_stream, device_index = 64, 1
+
+
+def test_stream_of_another_gpu():
+    """A stream belongs to one GPU: the call would run on the tensors' own current stream instead, unordered with it."""
+    with pytest.raises(ValueError, match="stream"):
+        M._elsewhere(0, OtherGpusStream(), lambda: None, ())
