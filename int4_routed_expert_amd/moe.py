@@ -17,6 +17,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 HEADERS = [os.path.join(os.path.dirname(_HERE), "include", h) for h in ("moe.h", "moe_dense.h")]
+HEADER = HEADERS[0]
 
 MOE_OK, MOE_EINVAL, MOE_ENULL, MOE_EDTYPE, MOE_EWORKSPACE, MOE_ENOSLOT, MOE_ESTALE, MOE_EHIP, MOE_ELEASE = \
     0, -1, -2, -3, -4, -5, -6, -7, -8

@@ -175,3 +175,9 @@ def test_stream_of_another_gpu():
     """A stream belongs to one GPU: the call would run on the tensors' own current stream instead, unordered with it."""
     with pytest.raises(ValueError, match="stream"):
         M._elsewhere(0, OtherGpusStream(), lambda: None, ())
+
+
+def test_header_names():
+    """moe.HEADER is include/moe.h, as it was before there were two headers."""
+    assert M.HEADER == M.HEADERS[0] and M.HEADER.endswith("moe.h")
+    assert "int moe_layer(" in open(M.HEADER).read()
