@@ -161,8 +161,8 @@ int moe_rope_freqs(int32_t rot, double theta, int32_t scaling, double scale, int
     if (scaling == MOE_ROPE_LINEAR) {
       freqs[i] = f / scale;
     } else if (scaling == MOE_ROPE_YARN) {
-      // high <= low (both ends at one index, or a trained length shorter than a turn): a step at low
-      const double slow = high > low ? std::min(std::max((i - low) / (high - low), 0.0), 1.0) : (i > low ? 1.0 : 0.0);
+      // high <= low: the blend lies before the first pair (high <= 0: every pair is slow) or beyond the last
+      const double slow = high > low ? std::min(std::max((i - low) / (high - low), 0.0), 1.0) : (high <= 0.0 ? 1.0 : 0.0);
       freqs[i] = f / scale * slow + f * (1.0 - slow);
     } else {
       freqs[i] = f;
