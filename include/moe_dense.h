@@ -38,8 +38,11 @@ extern "C" {
  * x, residual and h have x_dtype; the norm is that of the stored (rounded) h.  gamma:
  * [H] of g_dtype.  residual may be NULL (h = x); h, y and the pair q, d may each be NULL,
  * not all of them, and h needs a residual.  h may be residual or x, and y may be x, at
- * the same stride and in the same type (in place).  eps >= 0.  Statistics are fp32, added up in an order that
- * depends on H alone: a row's bits do not depend on the batch or on where it lies. */
+ * the same stride and in the same type (in place).  eps >= 0.  Squares are added up in fp32
+ * over eight neighbouring elements and in fp64 beyond (in fp64 throughout where H > 16384,
+ * or where they leave the range of fp32: a finite row of any magnitude has its norm), in an
+ * order that depends on H alone: a row's bits do not depend on the batch or on where it
+ * lies. */
 int moe_norm_quant(const void *x, int32_t x_dtype, int64_t ldx, const void *residual, int64_t ldr, const void *gamma,
                    int32_t g_dtype, float eps, int32_t S, int32_t H, void *h, int64_t ldh, void *y, int32_t y_dtype,
                    int64_t ldy, int8_t *q, int64_t ldq, float *d, void *stream);

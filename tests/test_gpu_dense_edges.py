@@ -1,0 +1,73 @@
+"""Dense operators on the GPU at the edges of their ranges, against 64-bit values.
+
+Tolerances, derived before the first run, in units of U = 2^-24 (half a step of fp32, relative); a result stored in bf16
+may be off by 2^-8 more.
+  norm   a lane's eight squares are added up in eight roundings, all later sums are fp64; half of that through the root;
+         the mean, eps, root, quotient (2) and the product with gamma one each: (8 / 2 + 6) U.  Far from 1 a row's
+         statistics are fp64 and its values scaled by a power of two: nothing more, except values that leave the range of
+         normal fp32 on the way, which are below 2^-60 of the largest.
+  codes  |q - v / d| <= 1/2 + 127 times twice the value's relative error (v and d both carry it).
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def M():
+    from int4_routed_expert_amd import moe
+    return moe
+
+
+def rng(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def check_rows(y, q, d, v, rel):
+    """y, and the int8 rows q, d, against 64-bit values v."""
+    more = 2.0 ** -8 if y.dtype == BF else 0.0
+    top = v.abs().amax(1, keepdim=True)
+    assert ((y.double() - v).abs() <= (rel + more) * v.abs() + top * 2.0 ** -60).all()
+    step = top[:, 0] / 127
+    assert ((d.double() - step).abs() <= (rel + U) * step).all()
+    assert ((q.double() - v / step[:, None]).abs() <= 0.5 + 127 * 2 * (rel + U)).all()
+
+
+# widths of every way to split a row over waves, for few rows and for many
+WIDTHS = [5, 500, 1000, 1001, 2048, 4096, 4099, 6144, 8192, 12288, 16384, 16385, 20000]
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("S", [3, 70])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_of_far_magnitudes(M, H, S, dtype):
+    """Rows whose squares leave the range of fp32 have the norm that the formula gives them, also beside ordinary rows."""
+    g = rng(H + S)
+    gamma = 1 + 0.2 * torch.randn(H, generator=g, device="cuda")
+    base = torch.randn(S, H, generator=g, device="cuda").clamp(-3, 3)
+    for scale in (1e19, 7e18, 1e25, 1e37, 1e-15, 1e-19, 1e-23, 1e-30, 1e-38):
+        x = (base * scale).to(dtype)
+        x[1] = base[1].to(dtype)
+        for eps in (0.0, 1e-40) if scale < 1 else (0.0, 1e-5):
+            for yd in (F32, BF):
+                _, y, q, d = M.norm_quant(x, gamma, eps, y_dtype=yd)
+                f, e = x.double(), torch.tensor(eps, dtype=F32).item()
+                check_rows(y, q, d, f / torch.sqrt((f * f).mean(1, keepdim=True) + e) * gamma.double(), (8 / 2 + 6) * U)
+
+
+@pytest.mark.parametrize("H", [700, 6144, 20000])
+def test_norm_of_one_large_value(M, H):
+    """One value whose square alone is beyond fp32, while the mean is not; zeros with eps = 0 stay NaN in their row."""
+    x = torch.randn(6, H, generator=rng(H), device="cuda")
+    x[2, H // 2] = 2e19
+    x[4] = 0
+    one = torch.ones(H, device="cuda")
+    _, y, q, d = M.norm_quant(x, one, 0.0, y_dtype=F32)
+    keep = [0, 1, 2, 3, 5]
+    f = x[keep].double()
+    check_rows(y[keep], q[keep], d[keep], f / torch.sqrt((f * f).mean(1, keepdim=True)), (8 / 2 + 6) * U)
+    assert torch.isnan(y[4]).all() and (q[4] == 0).all() and torch.isnan(d[4])
