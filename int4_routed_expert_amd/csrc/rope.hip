@@ -16,13 +16,15 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 1024;  // angles a workgroup may hold (8 KB of LDS)
 
-// Cosine and sine of pos * f, each within about 2^-24 of the true value for any position:
-// quarter turns are taken off in fp64, so the rest r, |r| <= pi / 4, is exact to the last
-// bit of fp32, where the Taylor series to r^9 and r^8 leave less than 2^-25.
+// Cosine and sine of pos * f, each within about 2^-23.5 of the true value while |pos * f| < 2^45
+// or so: quarter turns are taken off in fp64, from the product and its rounding error and by
+// pi / 2 in two parts, so the rest r, |r| <= pi / 4, is within 2^-50 before it is rounded to
+// fp32; there the Taylor series to r^9 and r^8 leave less than 2^-25.
 __device__ inline float2 cos_sin(double pos, double f) {
-  const double turns = pos * f * 0.63661977236758134308;  // 2 / pi
-  const double n = rint(turns);
-  const float r = (float)((turns - n) * 1.57079632679489661923);
+  const double a = pos * f;
+  const double n = rint(a * 0.63661977236758134308);  // 2 / pi
+  const double rest = fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489661923, a)) + fma(pos, f, -a);
+  const float r = (float)rest;
   const int quarter = (int)(int64_t)n & 3;
   const float r2 = r * r;
   const float s = fmaf(r * r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), r);

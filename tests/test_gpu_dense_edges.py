@@ -71,3 +71,50 @@ def test_norm_of_one_large_value(M, H):
     f = x[keep].double()
     check_rows(y[keep], q[keep], d[keep], f / torch.sqrt((f * f).mean(1, keepdim=True)), (8 / 2 + 6) * U)
     assert torch.isnan(y[4]).all() and (q[4] == 0).all() and torch.isnan(d[4])
+
+
+def exact_turns(pos, freqs):
+    """(cos, sin) of pos * f as float64 tensors [S, n], the product exact and reduced by pi to 90 digits (Machin's sum)."""
+    import math
+    from fractions import Fraction
+    one = 10 ** 90
+
+    def arctan_of_inverse(k):
+        total, term, n = 0, one // k, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= k * k
+            n += 2
+        return total
+    two_pi = Fraction(8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)), one)
+    c, s = [], []
+    for p in pos:
+        for f in freqs:
+            a = Fraction(p) * Fraction(f)
+            a -= round(a / two_pi) * two_pi
+            c.append(math.cos(a))
+            s.append(math.sin(a))
+    shape = len(pos), len(freqs)
+    return (torch.tensor(v, dtype=torch.float64, device="cuda").view(shape) for v in (c, s))
+
+
+FAR = [0, 1, 7, 100003, (1 << 24) + 1, (1 << 28) + 3, (1 << 31) - 1, -(1 << 31), (1 << 36) + 11, (1 << 40) + 3, -(1 << 44) - 5]
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_keeps_the_angles_of_far_positions(M, inter):
+    """The angle is the exact product of position and frequency, whatever its size.  A pair (1, 0) gives cosine and sine:
+    each within 2 U of the reduced angle's, the fused product of the other adds nothing, as the existing bound has it."""
+    freqs, _ = M.rope_freqs(64)
+    freqs[1] = 0.7364182
+    pos = torch.tensor(FAR, device="cuda")
+    x = torch.zeros(len(FAR), 3, 64, device="cuda")
+    (x[..., 0::2] if inter else x[..., :32]).fill_(1)
+    y, _ = M.rope(x, None, pos, freqs, interleaved=inter)
+    c, s = exact_turns(FAR, freqs.tolist())
+    got_c, got_s = (y[..., 0::2], y[..., 1::2]) if inter else (y[..., :32], y[..., 32:])
+    for got, want in ((got_c, c), (got_s, s)):
+        assert ((got.double() - want[:, None]).abs() <= 2 * U).all()
+    k = 7  # the positions that int32 holds
+    y32, _ = M.rope(x[:k], None, pos[:k].int(), freqs, interleaved=inter)
+    assert torch.equal(y32, y[:k])
