@@ -89,7 +89,7 @@ typedef struct moe_rope_tensor {
   int32_t heads;
 } moe_rope_tensor;
 int moe_rope(const moe_rope_tensor *q, const moe_rope_tensor *k, int32_t x_dtype, int32_t S, int32_t D, int32_t rot,
-             int32_t offset, int32_t layout, const void *pos, int32_t pos_i64, const double *freqs, float factor,
+             int32_t offset, int32_t layout, const void *pos, int32_t pos_i64, const double *freqs, double factor,
              void *stream);
 
 /* Frequencies for moe_rope (host): freqs[i] = theta^(-2 i / rot), i < rot / 2, scaled for
@@ -107,7 +107,7 @@ int moe_rope(const moe_rope_tensor *q, const moe_rope_tensor *k, int32_t x_dtype
  * trained_length >= 1 and beta_fast > beta_slow > 0 (the last two for MOE_ROPE_YARN). */
 enum moe_rope_scaling { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3 };
 int moe_rope_freqs(int32_t rot, double theta, int32_t scaling, double scale, int32_t trained_length, double beta_fast,
-                   double beta_slow, double *freqs, float *factor);
+                   double beta_slow, double *freqs, double *factor);
 
 #ifdef __cplusplus
 }

@@ -107,7 +107,7 @@ int moe_qmatmul(const int8_t *q, int64_t ldq, const float *d, const int8_t *w, i
 }
 
 int moe_rope(const moe_rope_tensor *q, const moe_rope_tensor *k, int32_t x_dtype, int32_t S, int32_t D, int32_t rot,
-             int32_t offset, int32_t layout, const void *pos, int32_t pos_i64, const double *freqs, float factor,
+             int32_t offset, int32_t layout, const void *pos, int32_t pos_i64, const double *freqs, double factor,
              void *stream) {
   if (S < 0 || D < 2 || D > 1024 || rot < 2 || rot % 2 || offset < 0 || offset > D - rot ||
       (layout != MOE_ROPE_HALF && layout != MOE_ROPE_INTERLEAVED) || (pos_i64 != 0 && pos_i64 != 1))
@@ -140,7 +140,7 @@ int moe_rope(const moe_rope_tensor *q, const moe_rope_tensor *k, int32_t x_dtype
 }
 
 int moe_rope_freqs(int32_t rot, double theta, int32_t scaling, double scale, int32_t trained_length, double beta_fast,
-                   double beta_slow, double *freqs, float *factor) {
+                   double beta_slow, double *freqs, double *factor) {
   if (rot < 2 || rot % 2 || !(theta > 1.0) || !std::isfinite(theta) || !(scale >= 1.0) || !std::isfinite(scale))
     return MOE_EINVAL;
   if (scaling < MOE_ROPE_PLAIN || scaling > MOE_ROPE_YARN || (scaling == MOE_ROPE_NTK && rot < 4)) return MOE_EINVAL;
@@ -168,7 +168,7 @@ int moe_rope_freqs(int32_t rot, double theta, int32_t scaling, double scale, int
       freqs[i] = f;
     }
   }
-  *factor = scaling == MOE_ROPE_YARN ? (float)(0.1 * std::log(scale) + 1.0) : 1.0f;
+  *factor = scaling == MOE_ROPE_YARN ? 0.1 * std::log(scale) + 1.0 : 1.0;
   return MOE_OK;
 }
 

@@ -55,7 +55,7 @@ struct QmmArgs {
 struct RopeArgs {
   bool stream;
   int S, D, half, offset, pos_i64;
-  float factor;
+  double factor;
   const void *pos;
   const double *freqs;
   moe_rope_tensor t[2];

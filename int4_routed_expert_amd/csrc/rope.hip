@@ -16,21 +16,27 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 1024;  // angles a workgroup may hold (8 KB of LDS)
 
-// Cosine and sine of pos * f, each within about 2^-23.5 of the true value while |pos * f| < 2^45
-// or so: quarter turns are taken off in fp64, from the product and its rounding error and by
-// pi / 2 in two parts, so the rest r, |r| <= pi / 4, is within 2^-50 before it is rounded to
-// fp32; there the Taylor series to r^9 and r^8 leave less than 2^-25.
-__device__ inline float2 cos_sin(double pos, double f) {
+// factor times cosine and sine of pos * f, rounded to fp32 once (within 2^-35 of the true
+// value before that) while |pos * f| < 2^45: quarter turns are taken off in fp64, from the
+// product and its rounding error and by pi / 2 in two parts, and the rest, |r| <= pi / 4, goes
+// through the Taylor series to r^11 and r^12 in fp64, whose next terms are below 2^-36.
+__device__ inline float2 cos_sin(double pos, double f, double factor) {
   const double a = pos * f;
   const double n = rint(a * 0.63661977236758134308);  // 2 / pi
-  const double rest = fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489661923, a)) + fma(pos, f, -a);
-  const float r = (float)rest;
+  const double r = fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489661923, a)) + fma(pos, f, -a);
   const int quarter = (int)(int64_t)n & 3;
-  const float r2 = r * r;
-  const float s = fmaf(r * r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), r);
-  const float c = fmaf(r2, fmaf(r2, fmaf(r2, fmaf(r2, 1.0f / 40320, -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
-  const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
-  return make_float2(quarter == 1 || quarter == 2 ? -cc : cc, quarter >= 2 ? -ss : ss);
+  const double r2 = r * r;
+  double s = fma(r2, -1. / 39916800, 1. / 362880), c = fma(r2, 1. / 479001600, -1. / 3628800);
+  s = fma(r2, s, -1. / 5040);
+  c = fma(r2, c, 1. / 40320);
+  s = fma(r2, s, 1. / 120);
+  c = fma(r2, c, -1. / 720);
+  s = fma(r2, s, -1. / 6);
+  c = fma(r2, c, 1. / 24);
+  s = fma(r * r2, s, r);
+  c = fma(r2, fma(r2, c, -0.5), 1.);
+  const double cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+  return make_float2((float)(factor * (quarter == 1 || quarter == 2 ? -cc : cc)), (float)(factor * (quarter >= 2 ? -ss : ss)));
 }
 
 typedef f32x4_t f32x4_w __attribute__((aligned(4)));
@@ -104,8 +110,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, RopePlan p) {
     const int t = i / a.half, k = i - t * a.half;
     const double pos = a.pos_i64 ? (double)ldg<int64_t>((const int64_t *)a.pos + s0 + t)
                                  : (double)ldg<int32_t>((const int32_t *)a.pos + s0 + t);
-    const float2 cs = cos_sin(pos, ldg<double>(a.freqs + k));
-    s_cs[i] = make_float2(cs.x * a.factor, cs.y * a.factor);
+    s_cs[i] = cos_sin(pos, ldg<double>(a.freqs + k), a.factor);
   }
   __syncthreads();
   const int heads = a.t[0].heads + a.t[1].heads;

@@ -107,8 +107,8 @@ def _load():
         "moe_silu_quant": (ctypes.c_int, [p, p, i32, i64, i32, i32, p, i32, i64, p, i64, p, p]),
         "moe_qmatmul_workspace_bytes": (i64, [p, i64, p, i64, i32, i32, i32]),
         "moe_qmatmul": (ctypes.c_int, [p, i64, p, p, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
-        "moe_rope": (ctypes.c_int, [p, p, i32, i32, i32, i32, i32, i32, p, i32, p, f32, p]),
-        "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f32)]),
+        "moe_rope": (ctypes.c_int, [p, p, i32, i32, i32, i32, i32, i32, p, i32, p, f64, p]),
+        "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f64)]),
         "moe_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_profile_report": (ctypes.c_int, [ctypes.c_char_p, sz]),
     }
@@ -381,7 +381,7 @@ def moe_rope_freqs(rot: int, theta: float, scaling: int, scale: float, trained_l
     import numpy as np
     _sizes("moe_rope_freqs", rot, trained_length)
     out = np.empty(max(rot, 0) // 2, np.float64)
-    factor = ctypes.c_float(0.0)
+    factor = ctypes.c_double(0.0)
     _check(_lib.moe_rope_freqs(rot, theta, scaling, scale, trained_length, beta_fast, beta_slow, ptr(out),
                                ctypes.byref(factor)), "moe_rope_freqs")
     return out, factor.value

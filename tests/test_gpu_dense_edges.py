@@ -8,6 +8,8 @@ may be off by 2^-8 more.
          normal fp32 on the way, which are below 2^-60 of the largest.
   codes  |q - v / d| <= 1/2 + 127 times twice the value's relative error (v and d both carry it).
 """
+import math
+
 import pytest
 import torch
 
@@ -75,7 +77,6 @@ def test_norm_of_one_large_value(M, H):
 
 def exact_turns(pos, freqs):
     """(cos, sin) of pos * f as float64 tensors [S, n], the product exact and reduced by pi to 90 digits (Machin's sum)."""
-    import math
     from fractions import Fraction
     one = 10 ** 90
 
@@ -118,3 +119,28 @@ def test_rope_keeps_the_angles_of_far_positions(M, inter):
     k = 7  # the positions that int32 holds
     y32, _ = M.rope(x[:k], None, pos[:k].int(), freqs, interleaved=inter)
     assert torch.equal(y32, y[:k])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("far", [1, 1 << 10, 1 << 16])
+def test_rope_coefficients_are_rounded_once(M, far, inter):
+    """A pair (1, 0) gives factor * (cos a, sin a): rounded to fp32 once, from a value within 2^-35 of the formula's (an fp64
+    series whose first term left out is below 2^-36 up to pi / 4; the angle itself is rounded at 2^-38 here)."""
+    S, n = 4096, 32
+    for factor in (1.0, 0.1 * math.log(4.0) + 1.0, 1.25):
+        freqs, _ = M.rope_freqs(2 * n)
+        pos = torch.randint(-far, far + 1, (S,), generator=rng(far), device="cuda")
+        x = torch.zeros(S, 1, 2 * n, device="cuda")
+        (x[..., 0::2] if inter else x[..., :n]).fill_(1)
+        y, _ = M.rope(x, None, pos, freqs, interleaved=inter, factor=factor)
+        a = pos.double()[:, None] * freqs
+        got_c, got_s = (y[..., 0::2], y[..., 1::2]) if inter else (y[..., :n], y[..., n:])
+        for got, want in ((got_c, a.cos() * factor), (got_s, a.sin() * factor)):
+            want = want[:, None]
+            assert ((got.double() - want).abs() <= U * want.abs() + factor * 2.0 ** -35).all()
+
+
+def test_yarn_factor_keeps_its_bits(M):
+    """The frequencies' factor comes as the fp64 value of its formula, and goes into the call as such."""
+    _, factor = M.rope_freqs(64, 10000.0, "yarn", 4.0, 4096)
+    assert abs(factor - (0.1 * math.log(4.0) + 1.0)) <= 2.0 ** -52
