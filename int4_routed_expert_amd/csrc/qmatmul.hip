@@ -293,7 +293,7 @@ __device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ mix_of(r))
 // One 16-byte load per lane from p straight into LDS, to lds + off + 16 lane (lds
 // wave-uniform, off a constant).
 __device__ inline __attribute__((always_inline)) void load_to_lds(const int8_t *p, uint32_t lds, int off) {
-  asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p), "i"(off) : "memory", "scc");
+  asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p), "i"(off) : "memory", "m0", "scc");
 }
 
 // Waits until at most N of this wave's loads are in flight and its reads of LDS are done,
