@@ -4,6 +4,8 @@ and the layer's own int8 activations next to the dense operators'."""
 import pytest
 import torch
 
+from tests.test_gpu_dense import check_rope
+
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
@@ -66,3 +68,47 @@ def test_second_turns_after_far_rows(M):
         step = v.abs().amax(1, keepdim=True) / 127
         assert ((d[p, None].double() - step).abs() <= 2.0 ** -19 * step).all()
         assert ((q[p].double() - v / step).abs() <= 0.5 + 127 * 2.0 ** -18).all()
+
+
+def pieces(S, heads, units):
+    """(tokens of a workgroup, workgroups) of the rotary kernel, from the rule in csrc/rope.hip for its widest units."""
+    tokens = max(1, min(256 // (heads * units), S // 1024))
+    return tokens, -(-S // tokens)
+
+
+@pytest.mark.parametrize("S,heads,D,units,tokens", [(GRID + 5, 2, 130, 65, 1), (2 * GRID + 7, 2, 1024, 64, 2)])
+@pytest.mark.parametrize("wide", [torch.int32, torch.int64])
+def test_rope_in_several_launches(M, S, heads, D, units, tokens, wide):
+    """The second launch goes on where the first ended, with its positions, inputs and outputs."""
+    assert pieces(S, heads, units)[0] == tokens and pieces(S, heads, units)[1] > GRID
+    g = rng(D)
+    # rows that overlap, 16 elements apart
+    x = torch.randn(S * 16 + heads * D, generator=g, device="cuda").bfloat16().as_strided((S, heads, D), (16, D, 1))
+    pos = torch.randint(0, 5000, (S,), generator=g, device="cuda", dtype=wide)
+    freqs, _ = M.rope_freqs(D)
+    y, _ = M.rope(x, None, pos, freqs)
+    cut = GRID * tokens
+    for p in (slice(0, 3), slice(cut - 5, cut + 9), slice(S - 3, S)):
+        check_rope(y[p], x[p], pos[p], freqs, 0, False, 1.0)
+        assert torch.equal(y[p], M.rope(x[p], None, pos[p], freqs)[0])
+
+
+@pytest.mark.parametrize("S,heads,kheads,D,rot,offset", [
+    (2049, 1, 1, 36, 36, 0), (5003, 2, 1, 64, 32, 32), (16383, 1, 1, 20, 12, 3), (4097, 1, 0, 24, 16, 8),
+    (3001, 3, 2, 32, 30, 2), (2051, 1, 1, 512, 512, 0), (20001, 1, 0, 2, 2, 0)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rope_of_several_tokens_a_workgroup(M, S, heads, kheads, D, rot, offset, inter, dtype):
+    """Few elements a token: a workgroup takes several, the last one fewer."""
+    g = rng(S + D)
+    both = torch.randn(S, heads + kheads, D, generator=g, device="cuda").to(dtype)
+    q, k = both[:, :heads], both[:, heads:] if kheads else None
+    pos = torch.randint(0, 100000, (S,), generator=g, device="cuda")
+    freqs, factor = M.rope_freqs(rot, 10000.0, "yarn", 4.0, 4096)
+    qo, ko = M.rope(q, k, pos, freqs, offset=offset, interleaved=inter, factor=factor)
+    check_rope(qo, q, pos, freqs, offset, inter, factor)
+    if kheads:
+        check_rope(ko, k, pos, freqs, offset, inter, factor)
+    # the same bits one token a workgroup
+    few, _ = M.rope(q[:700], None, pos[:700], freqs, offset=offset, interleaved=inter, factor=factor)
+    assert torch.equal(qo[:700], few)
