@@ -4,7 +4,7 @@ and the layer's own int8 activations next to the dense operators'."""
 import pytest
 import torch
 
-from tests.test_gpu_dense import check_rope
+from tests.test_gpu_dense import check_rope, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,38 @@ def test_rope_of_several_tokens_a_workgroup(M, S, heads, kheads, D, rot, offset,
     # the same bits one token a workgroup
     few, _ = M.rope(q[:700], None, pos[:700], freqs, offset=offset, interleaved=inter, factor=factor)
     assert torch.equal(qo[:700], few)
+
+
+COPIES = [  # kernel, S, N, K, whether q and w lie on 16-byte boundaries
+    ("few", 17, 40, 528, 0, 1), ("few", 40, 40, 272, 1, 0), ("few32", 200, 500, 272, 0, 1), ("few32", 200, 500, 272, 1, 0),
+    ("tile32", 17, 6200, 4112, 0, 1), ("tile32", 700, 300, 4112, 1, 0), ("tile32", 500, 500, 4112, 0, 0),
+    ("tile32x64", 130, 2100, 2064, 0, 1), ("tile32x64", 500, 900, 1552, 1, 0), ("tile32x64", 1540, 300, 1552, 0, 0),
+    ("tile64", 130, 4100, 1040, 0, 1), ("tile64", 500, 1500, 1040, 1, 0), ("tile64", 1540, 500, 1040, 0, 0),
+    ("tile64x128", 1030, 1500, 1552, 0, 1), ("tile64x128", 1030, 1500, 1552, 1, 0), ("tile64x128", 200, 6200, 1552, 0, 0),
+    ("tile128", 500, 6200, 528, 0, 1), ("tile128", 1030, 3000, 528, 1, 0), ("tile128", 2050, 1500, 528, 0, 0),
+    ("tile128x2", 2050, 3000, 272, 0, 1), ("tile128x2", 3000, 2100, 272, 1, 0), ("tile128x2", 700, 8200, 272, 0, 0),
+    ("tile256", 2050, 6200, 1040, 0, 1), ("tile256", 3000, 4100, 1040, 1, 0), ("tile256", 3000, 4100, 1040, 0, 0),
+]
+
+
+@pytest.mark.parametrize("kernel,S,N,K,q16,w16", COPIES)
+def test_product_copies_the_operand_that_needs_it(M, kernel, S, N, K, q16, w16):
+    """Tokens, weights or both away from 16-byte boundaries: the tile kernels run behind a copy of just those."""
+    g = rng(S + N + K)
+    q, d, _, _ = operands(g, S, 1, K, *((0, 0) if q16 else (5, 3)))
+    _, _, w, dw = operands(g, 1, N, K, *((0, 0) if w16 else (7, 1)))
+    rows = (0 if q16 else S) + (0 if w16 else N)
+    need = M.moe_qmatmul_workspace_bytes(q, q.stride(0), w, w.stride(0), S, N, K)
+    assert need == (rows * K if kernel.startswith("tile") else 0)
+    ws = torch.full((need + 64,), 99, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    M.moe_profile_enable(True)
+    try:
+        y = M.qmatmul(q, d, w, dw, out_dtype=F32, ws=ws[:need] if need else None)
+        ran = set(M.moe_profile_report())
+    finally:
+        M.moe_profile_enable(False)
+    assert ran == {"qmatmul_" + kernel} | ({"qmatmul_align"} if need else set())
+    assert (ws[need:] == 99).all()
+    want = (q.double() @ w.double().t().contiguous()).round().float() * (d[:, None] * dw)  # exact sums under 2^53
+    assert torch.equal(y, want)
