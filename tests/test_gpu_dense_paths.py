@@ -1,6 +1,7 @@
 """Paths of the dense operators that only certain sizes and places take, each named by the test that takes it:
 workgroups that go on to a second row, launches in several pieces, copies of one operand, several tokens a workgroup,
 and the layer's own int8 activations next to the dense operators'."""
+import numpy as np
 import pytest
 import torch
 
@@ -147,3 +148,36 @@ def test_product_copies_the_operand_that_needs_it(M, kernel, S, N, K, q16, w16):
     assert (ws[need:] == 99).all()
     want = (q.double() @ w.double().t().contiguous()).round().float() * (d[:, None] * dw)  # exact sums under 2^53
     assert torch.equal(y, want)
+
+
+def test_the_layers_int8_activations(M):
+    """moe_ffn with act_int8 and int8 weights, next to the same experts put together from the dense operators: it
+    quantises the norm's fp32 rows to the norm's own int8 rows.  All sums of integers are exact; the scales' products may
+    be rounded in another order, which moves an element of h that lies on a rounding border by one step (a few 1e-3 of
+    the output at most: the bars of the layer's own int8 tests, 5e-3 at most and 1e-5 for the median token)."""
+    from gen import inputs as gen
+    from tests.devlayer import DeviceLayer
+    w = gen.WORKLOADS["tiny"]
+    w = w.with_(cfg=gen.LayerConfig(**{**w.cfg.__dict__, "weight_format": 2}))
+    dl = DeviceLayer(w, host_experts=True, mfma_min_tokens=0, act_int8=1)
+    c, S = dl.c, 37
+    x0 = torch.randn(S, c.hidden, generator=rng(3), device="cuda") * 3
+    _, x, q, d = M.norm_quant(x0, 1 + 0.2 * torch.rand(c.hidden, generator=rng(4), device="cuda"), 1e-5, y_dtype=F32)
+    idx, wt = dl.route(x, M.MOE_F32)
+    got = dl.ffn(x, M.MOE_F32, idx, wt)
+
+    def expert(e):
+        i8 = lambda a: torch.from_numpy(np.ascontiguousarray(a).view(np.int8)).cuda()  # noqa: E731
+        h = dl.host_expert(e)
+        qg, sg, qu, su, qd, sd = h.parts()
+        gate, up = (M.qmatmul(q, d, i8(a).view(h.inter, c.hidden), torch.from_numpy(b).cuda().float().view(-1), out_dtype=F32)
+                    for a, b in ((qg, sg), (qu, su)))
+        _, hq, hd = M.silu_quant(gate, up)
+        return M.qmatmul(hq, hd, i8(qd).view(c.hidden, h.inter), torch.from_numpy(sd).cuda().float().view(-1), out_dtype=F32)
+    want = expert(c.n_experts).double() if c.shared_inter > 0 else torch.zeros(S, c.hidden, dtype=torch.float64, device="cuda")
+    for e in range(c.n_experts):
+        share = (wt * (idx == e)).sum(1)
+        if share.any():
+            want += share[:, None].double() * expert(e).double()
+    errs = (got.double() - want).abs().amax(1) / want.abs().amax(1)
+    assert errs.max() <= 5e-3 and errs.median() <= 1e-5
