@@ -594,7 +594,6 @@ _ROPE_SCALING = {"none": MOE_ROPE_PLAIN, "linear": MOE_ROPE_LINEAR, "ntk": MOE_R
 def rope_freqs(rot: int, theta: float = 10000.0, scaling: str = "none", scale: float = 1.0, trained_length: int = 0,
                beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
     """(freqs, factor) for rope: moe_rope_freqs with the frequencies as a float64 tensor on `device`."""
-    import torch
     if scaling not in _ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}, not {scaling!r}")
     f, factor = moe_rope_freqs(rot, theta, _ROPE_SCALING[scaling], scale, trained_length, beta_fast, beta_slow)
@@ -614,10 +613,12 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
     or int64 and freqs [rot / 2] float64, into tensors allocated on q's GPU, or over q and k with inplace=True."""
     dtype = q.dtype
     xd = _code(dtype, "q")
-    S, D = q.shape[0], q.shape[-1]
-    strides = [_heads(q, S, D, "q"), None]
+    shape = q.shape
+    S, D = shape[0], shape[-1]
+    strides, counts = [_heads(q, S, D, "q"), None], [shape[1], 0]
     if k is not None:
         strides[1] = _heads(k, S, D, "k")
+        counts[1] = k.shape[1]
         if k.dtype != dtype:
             raise ValueError(f"k must have q's type {dtype}, not {k.dtype}")
     wide = pos.dtype == torch.int64
@@ -626,7 +627,8 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
     _vector(pos, S, pos.dtype, "pos")
     half = freqs.shape[0] if freqs.dim() == 1 else -1
     _vector(freqs, half, torch.float64, "freqs")
-    _sizes("moe_rope", S, D, 2 * half, offset, q.shape[1], 0 if k is None else k.shape[1])
+    if (S | D | 2 * half | offset | counts[0] | counts[1]) >> 31:
+        _sizes("moe_rope", S, D, 2 * half, offset, *counts)
     gpu = _gpu(q, k, pos, freqs)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, rope, (q, k, pos, freqs), q, k, pos, freqs, offset, interleaved, factor, inplace)
@@ -636,7 +638,7 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
             continue
         o = outs[i] = t if inplace else _empty_like(t, memory_format=_ROWS)
         s0, s1, _ = strides[i]
-        heads = t.shape[1]
+        heads = counts[i]
         o0, o1 = (s0, s1) if inplace else (heads * D, D)
         args[i] = _ROPE_TENSOR.pack(t.data_ptr(), o.data_ptr(), s0, s1, o0, o1, heads)
     rc = _lib.moe_rope(args[0], args[1], xd, S, D, 2 * half, offset,
