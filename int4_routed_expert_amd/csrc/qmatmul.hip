@@ -3,14 +3,19 @@
 // (plan_of): a dot-product kernel for up to four tokens (eight where weight rows are few and
 // long), a direct matrix-core kernel for few tokens or small operands, LDS tiles for the
 // others.  Measured (bf16 outputs):
-//   1 x 4096 x 6144 (S x N x K)   5.8 us, 4.3 TB/s; 1 x 12288 x 6144 12.4 us, 6.1 TB/s (a
+//   1 x 4096 x 6144 (S x N x K)   5.9 us, 4.3 TB/s; 1 x 12288 x 6144 12.4 us, 6.1 TB/s (a
 //                                 copy of 1 GiB runs at 5.1): bound by the weights' bytes
-//   256 x 6144 x 6144             18 us, 1.07 POP/s: a compute unit takes in about 80 KB/us
-//                                 past its XCD's L2, and the tiles move 1.2 MB through each
-//   8192 x 12288 x 6144           510 to 545 us on different cards, 2.27 to 2.43 POP/s (a
+//   256 x 6144 x 6144             18 us, 1.07 POP/s: 192 tiles leave a quarter of the 256
+//                                 compute units idle, and the others take in 1.2 MB each at
+//                                 76 KB/us (77% of it hits in its XCD's L2, which alone
+//                                 would give 120)
+//   8192 x 12288 x 6144           510 to 550 us on different cards, 2.25 to 2.43 POP/s (a
 //                                 library int8 product: 2.04): the matrix cores are busy
-//                                 61% of the cycles, and the chip clocks down to 1.8 GHz to
-//                                 stay within its power (all operands zero: 484 us)
+//                                 62% of the cycles; a SIMD has one wave, which waits at a
+//                                 barrier every 128 bytes of K, and the chip clocks down to
+//                                 1.8 GHz to stay within its power (all operands zero: 484)
+// Outputs of a width that is no multiple of 4 are stored element by element and not past the
+// caches: 8192 x 12287 x 6144 586 us, 256 x 6143 x 6144 18.5.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -542,10 +547,14 @@ struct QmmPlan {
   int64_t bytes_q, bytes;  // workspace: of the token rows, of all
 };
 
-// The kernel with the least estimated time, from times measured over 60 shapes (us).  A
-// tile kernel: 2.5, and for each round of 256 tiles (one a compute unit) a part for its
-// start and end and a part for every 128 of K (both with `together` tiles on a unit), or the time in which one tile alone gets
-// through K.  The direct kernel: 2.3, and each workgroup moves 39 KB/us.
+// The kernel with the least estimated time, fitted to measured ones (us).  A tile kernel:
+// 2.5, and for each round of 256 tiles (one a compute unit) a part for its start and end and
+// a part for every 128 of K (both with `together` tiles on a unit), or the time in which one
+// tile alone gets through K.  The direct kernel: 2.3, and each workgroup moves 39 KB/us.  Of
+// 62 shapes measured with every kernel the rule takes the best or one within 7% of it, but
+// for a short K with many outputs, whose stores the estimates do not know: 256 x 6144 x 2048
+// 11.1 us against 9.2, 512 x 6144 x 2048 14.9 against 13.5, 2048 x 6144 x 2048 37 to 46
+// against 37, 4096 x 512 x 144 11.4 against 5.2; and 4 x 4096 x 512, below.
 QmmPlan plan_of(const QmmArgs &a) {
   QmmPlan p{};
   const bool q16 = on16(a.q, a.ldq, a.S, a.K), w16 = on16(a.w, a.ldw, a.N, a.K);

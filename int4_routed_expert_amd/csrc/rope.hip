@@ -5,7 +5,8 @@
 // tokens (a part of one token's heads where there are few tokens), forms their sines and
 // cosines once in LDS, a pair a thread, and streams the heads in units of 16 bytes (two
 // elements or one where the sizes ask for it).  8192 tokens, 72 heads of 128, bf16: 54 us,
-// 5.6 TB/s (interleaved 56; a copy of 1 GiB runs at 5.1).
+// 5.6 TB/s (interleaved 56; a copy of 1 GiB runs at 5.1).  Units of one element cost a load
+// and a store each: 4096 tokens, 34 heads of 129, 40 us, of 128 16 us.
 #include <algorithm>
 
 #include "dense.h"

@@ -7,7 +7,9 @@
 // Measured: norm 8192 x 6144 bf16 with residual, norm and int8 rows 97 us, 4.7 TB/s (fp32
 // in: 132 us, 5.7); SwiGLU 4096 x 12288 bf16 63 us, 4.0 TB/s (fp32: 85 us, 5.3; a copy of 1
 // GiB runs at 5.1): in bf16 the exponential and the divisions take about as long as the
-// memory.  One row of 6144: 4.7 us, two barriers and a trip to memory.
+// memory.  One row of 6144: 4.6 us, two barriers and a trip to memory.  Rows away from
+// 16-byte boundaries: norm 4096 x 5001 bf16 69 us (5000 wide: 49), bound by its stores at odd
+// places; SwiGLU 32 (31).
 #include <algorithm>
 
 #include "dense.h"
@@ -86,7 +88,9 @@ __device__ inline float far_root_of(double sum, const RowArgs &a, float &scale) 
 }
 
 // Rows of any length: the row is read once for the statistics and again for each
-// output; a thread meets the same elements in every pass, so outputs may be inputs.
+// output; a thread meets the same elements in every pass, so outputs may be inputs.  One
+// element at a time by one workgroup a row, bound by that: norm 2000 x 20000 bf16 with
+// residual 365 us, 1.0 TB/s (2 x 20000: 74 us), SwiGLU 121 us, 1.7 TB/s.
 template <RowOp OP, bool BF16>
 __global__ __launch_bounds__(kRowThreads) void k_rows_long(RowArgs a) {
   __shared__ double s_sum[kRowThreads / 64];
@@ -296,8 +300,10 @@ struct Codes : Divisor {
 // (8 x 2: registers for three workgroups on a compute unit, 65 us against 72 for norm 4096
 // x 8192.  Norm with one block a wave: for eight waves a SIMD, 23.0 us against 23.9 for
 // 16384 rows of 333 bf16.)
+template <RowOp OP, int W, int IT>
+constexpr int kRowWaves = W == 8 && IT == 2 ? 6 : OP == kNorm && W <= 4 && IT == 1 ? 8 : 1;
 template <RowOp OP, bool BF16, int W, int IT, bool ON16>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W == 8 && IT == 2 ? 6 : OP == kNorm && W <= 4 && IT == 1 ? 8 : 1) void k_rows(RowArgs a) {
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, kRowWaves<OP, W, IT>) void k_rows(RowArgs a) {
   // each row of a workgroup's turn uses the other half, so one barrier orders both uses
   __shared__ __align__(16) double s_sum[2][W * IT];
   __shared__ __align__(16) uint32_t s_max[2][W];

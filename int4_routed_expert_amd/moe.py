@@ -70,8 +70,7 @@ def _load():
     # torch ships its own HIP runtime and loads it by path.  Loaded first, the
     # library would resolve libamdhip64.so.7 through its run path to a second
     # runtime in the same process, which sees no device and knows none of
-    # torch's streams; with torch loaded first, the soname binds to torch's copy.
-    import torch  # noqa: F401
+    # torch's streams; with torch loaded first (above), the soname binds to torch's copy.
     L = ctypes.CDLL(LIB_PATH)
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     f32, f64 = ctypes.c_float, ctypes.c_double
@@ -333,6 +332,8 @@ _empty_like = torch.empty_like
 
 
 # ---- dense operators ---------------------------------------------------------------------------------------------------
+# They serve: no call has a backward pass, and the allocating ones refuse inputs that ask for gradients while torch records
+# them.  A tensor written over (norm_quant's h, rope's inplace) raises its version.
 # The ABI's sizes are int32, and ctypes would pass on the low 32 bits of a larger one.
 
 def _sizes(where: str, *sizes) -> None:

@@ -105,7 +105,7 @@ FAR = [0, 1, 7, 100003, (1 << 24) + 1, (1 << 28) + 3, (1 << 31) - 1, -(1 << 31),
 @pytest.mark.parametrize("inter", [False, True])
 def test_rope_keeps_the_angles_of_far_positions(M, inter):
     """The angle is the exact product of position and frequency, whatever its size.  A pair (1, 0) gives cosine and sine:
-    each within 2 U of the reduced angle's, the fused product of the other adds nothing, as the existing bound has it."""
+    each within 2 U of the true value (the zero beside them adds nothing)."""
     freqs, _ = M.rope_freqs(64)
     freqs[1] = 0.7364182
     pos = torch.tensor(FAR, device="cuda")
