@@ -303,7 +303,7 @@ struct Codes : Divisor {
 template <RowOp OP, int W, int IT>
 constexpr int kRowWaves = W == 8 && IT == 2 ? 6 : OP == kNorm && W <= 4 && IT == 1 ? 8 : 1;
 template <RowOp OP, bool BF16, int W, int IT, bool ON16>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, kRowWaves<OP, W, IT>) void k_rows(RowArgs a) {
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, (kRowWaves<OP, W, IT>)) void k_rows(RowArgs a) {
   // each row of a workgroup's turn uses the other half, so one barrier orders both uses
   __shared__ __align__(16) double s_sum[2][W * IT];
   __shared__ __align__(16) uint32_t s_max[2][W];
