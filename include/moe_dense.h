@@ -75,7 +75,7 @@ int moe_qmatmul(const int8_t *q, int64_t ldq, const float *d, const int8_t *w, i
  * (MOE_ROPE_HALF).  Pair i of token s turns by a = pos[s] * freqs[i]:
  *   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a).
  * a is the whole product, reduced in fp64 with what its rounding leaves off, so far
- * positions lose nothing (|a| < 2^45, |pos| <= 2^53).  q: [S, heads, D] and
+ * positions lose nothing (|a| < 2^62; beyond 2^53 a position counts as the nearest fp64).  q: [S, heads, D] and
  * k: [S, kheads, D] of x_dtype (k may be NULL with kheads = 0), both turned in the same
  * launch, each with its own token stride and head stride; q_out and k_out likewise.
  * Dimensions outside the part are copied, or left alone where an output is its input

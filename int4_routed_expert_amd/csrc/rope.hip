@@ -18,14 +18,17 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 1024;  // angles a workgroup may hold (8 KB of LDS)
 
 // factor times cosine and sine of pos * f, rounded to fp32 once (within 2^-35 of the true
-// value before that) while |pos * f| < 2^45: quarter turns are taken off in fp64, from the
-// product and its rounding error and by pi / 2 in two parts, and the rest, |r| <= pi / 4, goes
+// value before that) for |pos * f| < 2^62: quarter turns are taken off in fp64, from the
+// product and its rounding error and by pi / 2 in two parts, a second time for those that the
+// first estimate of their number missed (from 2^49 on), and the rest, |r| <= pi / 4, goes
 // through the Taylor series to r^11 and r^12 in fp64, whose next terms are below 2^-36.
 __device__ inline float2 cos_sin(double pos, double f, double factor) {
   const double a = pos * f;
   const double n = rint(a * 0.63661977236758134308);  // 2 / pi
-  const double r = fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489661923, a)) + fma(pos, f, -a);
-  const int quarter = (int)(int64_t)n & 3;
+  const double r0 = fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489661923, a)) + fma(pos, f, -a);
+  const double m = rint(r0 * 0.63661977236758134308);
+  const double r = fma(-m, 1.57079632679489661923, r0);
+  const int quarter = ((int)(int64_t)n + (int)m) & 3;
   const double r2 = r * r;
   double s = fma(r2, -1. / 39916800, 1. / 362880), c = fma(r2, 1. / 479001600, -1. / 3628800);
   s = fma(r2, s, -1. / 5040);

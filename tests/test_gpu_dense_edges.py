@@ -100,6 +100,7 @@ def exact_turns(pos, freqs):
 
 
 FAR = [0, 1, 7, 100003, (1 << 24) + 1, (1 << 28) + 3, (1 << 31) - 1, -(1 << 31), (1 << 36) + 11, (1 << 40) + 3, -(1 << 44) - 5]
+FARTHEST = [(1 << 49) + 1, -(1 << 50) - 3, (1 << 53) - 1, 5 << 52, -(7 << 56), (1 << 61) + (1 << 20), -(1 << 62) + (1 << 30)]
 
 
 @pytest.mark.parametrize("inter", [False, True])
@@ -116,6 +117,13 @@ def test_rope_keeps_the_angles_of_far_positions(M, inter):
     got_c, got_s = (y[..., 0::2], y[..., 1::2]) if inter else (y[..., :32], y[..., 32:])
     for got, want in ((got_c, c), (got_s, s)):
         assert ((got.double() - want[:, None]).abs() <= 2 * U).all()
+    far = torch.tensor(FARTHEST, device="cuda")  # all of them fp64 values
+    y2, _ = M.rope(x[:len(FARTHEST)], None, far, freqs[:2].contiguous(), interleaved=inter)
+    c, s = exact_turns(FARTHEST, freqs[:2].tolist())
+    got_c, got_s = (y2[..., 0:4:2], y2[..., 1:4:2]) if inter else (y2[..., :2], y2[..., 2:4])
+    x1, x2 = (x[0, 0, 0:4:2], x[0, 0, 1:4:2]) if inter else (x[0, 0, :2], x[0, 0, 2:4])
+    for got, want in ((got_c, c * x1 - s * x2), (got_s, c * x2 + s * x1)):
+        assert ((got.double() - want[:, None]).abs() <= 4 * U).all()
     k = 7  # the positions that int32 holds
     y32, _ = M.rope(x[:k], None, pos[:k].int(), freqs, interleaved=inter)
     assert torch.equal(y32, y[:k])
