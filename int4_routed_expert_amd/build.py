@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["abi.cpp", "pool.cpp", "route.hip", "ffn_gemv.hip", "ffn_mfma.hip", "pack.hip", "dense.cpp", "rows.hip",
-           "rope.hip", "qmatmul.hip"]
+           "rope.hip", "qmatmul.hip", "experts.cpp", "mx.hip", "products.hip", "dispatch.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-fp32 VALU instructions stay disabled for every device compile.

@@ -153,47 +153,6 @@ __device__ inline int col_of(int tid, int it) {
   return (it * W + (tid >> 6)) * 512 + (tid & 63) * 8;
 }
 
-typedef u32x4_t u32x4_w __attribute__((aligned(4)));
-typedef u32x4_t u32x4_h __attribute__((aligned(2)));
-typedef f32x4_t f32x4_w __attribute__((aligned(4)));
-typedef uint64_t u64_b __attribute__((aligned(1)));
-
-// Eight neighbours.  A bf16 row that starts in the middle of a word is read as the words
-// that hold the eight (each holds at least one of them), shifted together: loads from
-// odd places take the hardware several times as long.
-template <bool BF16, bool ON16>
-__device__ inline void load8(const void *p, int64_t i, float *v) {
-  if constexpr (BF16) {
-    const uint16_t *q = (const uint16_t *)p + i;
-    uint32_t d[4];
-    if constexpr (ON16) {
-      const uint4 r = ldg<uint4>(q);
-      d[0] = r.x; d[1] = r.y; d[2] = r.z; d[3] = r.w;
-    } else {
-      const uint32_t sh = (uint32_t)(uintptr_t)q & 2;
-      const u32x4_t r = *(const __attribute__((address_space(1))) u32x4_w *)((uintptr_t)q & ~(uintptr_t)3);
-      const uint32_t e = ldg<uint32_t>((const void *)((uintptr_t)(q + 7) & ~(uintptr_t)3));
-      d[0] = __builtin_amdgcn_alignbyte(r.y, r.x, sh);
-      d[1] = __builtin_amdgcn_alignbyte(r.z, r.y, sh);
-      d[2] = __builtin_amdgcn_alignbyte(r.w, r.z, sh);
-      d[3] = __builtin_amdgcn_alignbyte(e, r.w, sh);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(d[j] << 16);
-      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
-    }
-  } else {
-    const float *q = (const float *)p + i;
-    const f32x4_t r0 = *(const __attribute__((address_space(1))) f32x4_w *)q;
-    const f32x4_t r1 = *(const __attribute__((address_space(1))) f32x4_w *)(q + 4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = r0[j];
-      v[4 + j] = r1[j];
-    }
-  }
-}
 template <bool BF16, bool ON16>
 __device__ inline void store8(void *p, int64_t i, const float *v, bool stream) {
   if constexpr (BF16) {

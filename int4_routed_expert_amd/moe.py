@@ -1,4 +1,4 @@
-"""Python binding of ``libmoe.so`` (include/moe.h, include/moe_dense.h): argument marshalling only.
+"""Python binding of ``libmoe.so`` (include/moe.h, moe_dense.h, moe_mx.h, moe_grouped.h): argument marshalling only.
 
 Every function with a ``moe_`` name calls the C entry point of the same name.
 Tensors are passed as raw pointers (``torch.Tensor.data_ptr()`` for device
@@ -16,7 +16,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
-HEADERS = [os.path.join(os.path.dirname(_HERE), "include", h) for h in ("moe.h", "moe_dense.h")]
+HEADERS = [os.path.join(os.path.dirname(_HERE), "include", h) for h in ("moe.h", "moe_dense.h", "moe_mx.h", "moe_grouped.h")]
 HEADER = HEADERS[0]
 
 MOE_OK, MOE_EINVAL, MOE_ENULL, MOE_EDTYPE, MOE_EWORKSPACE, MOE_ENOSLOT, MOE_ESTALE, MOE_EHIP, MOE_ELEASE = \
@@ -24,6 +24,7 @@ MOE_OK, MOE_EINVAL, MOE_ENULL, MOE_EDTYPE, MOE_EWORKSPACE, MOE_ENOSLOT, MOE_ESTA
 MOE_F32, MOE_BF16 = 0, 1
 MOE_WF_Q4_G32, MOE_WF_Q4_ROW, MOE_WF_Q8_ROW = 0, 1, 2
 MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+MOE_MX_FLOOR, MOE_MX_UP = 0, 1
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_NTK, MOE_ROPE_YARN = 0, 1, 2, 3
 
 
@@ -62,6 +63,16 @@ class moe_rope_tensor(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_token", ctypes.c_int64),
                 ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
                 ("heads", ctypes.c_int32)]
+
+
+class moe_mx_rows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("e", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("lde", ctypes.c_int64),
+                ("expert_q", ctypes.c_int64), ("expert_e", ctypes.c_int64)]
+
+
+class moe_groups(ctypes.Structure):
+    _fields_ = [("first", ctypes.c_void_p), ("order", ctypes.c_void_p), ("n", ctypes.c_int32),
+                ("top_k", ctypes.c_int32)]
 
 
 def _load():
@@ -108,6 +119,18 @@ def _load():
         "moe_qmatmul": (ctypes.c_int, [p, i64, p, p, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
         "moe_rope": (ctypes.c_int, [p, p, i32, i32, i32, i32, i32, i32, p, i32, p, f64, p]),
         "moe_rope_freqs": (ctypes.c_int, [i32, f64, i32, f64, i32, f64, f64, p, ctypes.POINTER(f64)]),
+        "moe_mx_quant": (ctypes.c_int, [p, i32, i64, i32, i32, i32, p, i64, p, i64, p]),
+        "moe_mx_silu_quant": (ctypes.c_int, [p, p, i32, i64, i32, i32, i32, p, i64, p, i64, p]),
+        "moe_mx_values": (ctypes.c_int, [p, i64, p, i64, i32, i32, p, i32, i64, p]),
+        "moe_mx_matmul_workspace_bytes": (i64, [p, p, i32, i32, i32]),
+        "moe_mx_matmul": (ctypes.c_int, [p, p, i32, i32, i32, p, i32, i64, p, sz, p]),
+        "moe_group_workspace_bytes": (i64, [i32, i32, i32]),
+        "moe_group": (ctypes.c_int, [p, i32, i32, i32, p, p, p, p, sz, p]),
+        "moe_grouped_matmul_workspace_bytes": (i64, [p, i64, i32, p, i64, i64, p, i32, i32, i32]),
+        "moe_grouped_matmul": (ctypes.c_int, [p, i64, i32, p, i64, i64, p, i32, i32, i32, p, i32, i64, p, sz, p]),
+        "moe_mx_grouped_matmul_workspace_bytes": (i64, [p, i32, p, p, i32, i32, i32]),
+        "moe_mx_grouped_matmul": (ctypes.c_int, [p, i32, p, p, i32, i32, i32, p, i32, i64, p, sz, p]),
+        "moe_combine": (ctypes.c_int, [p, i32, i64, i32, p, p, i32, i32, i32, p, i64, p, i32, i64, p]),
         "moe_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "moe_profile_report": (ctypes.c_int, [ctypes.c_char_p, sz]),
     }
@@ -652,6 +675,376 @@ def rope(q, k, pos, freqs, offset: int = 0, interleaved: bool = False, factor: f
         if k is not None:
             _written(k)
     return outs[0], outs[1]
+
+
+# ---- microscaled rows, products grouped by expert -----------------------------------------------------------------------
+# They serve too: no backward pass, inputs that require gradients are refused.
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def moe_mx_quant(x, x_dtype: int, ldx: int, S: int, H: int, rounding: int, q, ldq: int, e, lde: int, stream=None) -> None:
+    _sizes("moe_mx_quant", S, H)
+    _check(_lib.moe_mx_quant(ptr(x), x_dtype, ldx, S, H, rounding, ptr(q), ldq, ptr(e), lde, stream_handle(stream)),
+           "moe_mx_quant")
+
+
+def moe_mx_silu_quant(g, u, x_dtype: int, ldx: int, S: int, I: int, rounding: int, q, ldq: int, e, lde: int,
+                      stream=None) -> None:
+    _sizes("moe_mx_silu_quant", S, I)
+    _check(_lib.moe_mx_silu_quant(ptr(g), ptr(u), x_dtype, ldx, S, I, rounding, ptr(q), ldq, ptr(e), lde,
+                                  stream_handle(stream)), "moe_mx_silu_quant")
+
+
+def moe_mx_values(q, ldq: int, e, lde: int, S: int, H: int, y, y_dtype: int, ldy: int, stream=None) -> None:
+    _sizes("moe_mx_values", S, H)
+    _check(_lib.moe_mx_values(ptr(q), ldq, ptr(e), lde, S, H, ptr(y), y_dtype, ldy, stream_handle(stream)), "moe_mx_values")
+
+
+def moe_mx_matmul_workspace_bytes(x: moe_mx_rows, w: moe_mx_rows, S: int, N: int, B: int) -> int:
+    _sizes("moe_mx_matmul_workspace_bytes", S, N, B)
+    return _lib.moe_mx_matmul_workspace_bytes(_ref(x), _ref(w), S, N, B)
+
+
+def moe_mx_matmul(x: moe_mx_rows, w: moe_mx_rows, S: int, N: int, B: int, y, y_dtype: int, ldy: int, ws, ws_bytes: int,
+                  stream=None) -> None:
+    _sizes("moe_mx_matmul", S, N, B)
+    _check(_lib.moe_mx_matmul(_ref(x), _ref(w), S, N, B, ptr(y), y_dtype, ldy, ptr(ws), ws_bytes, stream_handle(stream)),
+           "moe_mx_matmul")
+
+
+def moe_group_workspace_bytes(S: int, k: int, E: int) -> int:
+    _sizes("moe_group_workspace_bytes", S, k, E)
+    return _lib.moe_group_workspace_bytes(S, k, E)
+
+
+def moe_group(idx, S: int, k: int, E: int, first, order, place, ws, ws_bytes: int, stream=None) -> None:
+    _sizes("moe_group", S, k, E)
+    _check(_lib.moe_group(ptr(idx), S, k, E, ptr(first), ptr(order), ptr(place), ptr(ws), ws_bytes, stream_handle(stream)),
+           "moe_group")
+
+
+def moe_grouped_matmul_workspace_bytes(x, ldx: int, x_rows: int, w, ldw: int, expert: int, g: moe_groups, T: int, N: int,
+                                       K: int) -> int:
+    _sizes("moe_grouped_matmul_workspace_bytes", x_rows, T, N, K)
+    return _lib.moe_grouped_matmul_workspace_bytes(ptr(x), ldx, x_rows, ptr(w), ldw, expert, _ref(g), T, N, K)
+
+
+def moe_grouped_matmul(x, ldx: int, x_rows: int, w, ldw: int, expert: int, g: moe_groups, T: int, N: int, K: int, y,
+                       y_dtype: int, ldy: int, ws, ws_bytes: int, stream=None) -> None:
+    _sizes("moe_grouped_matmul", x_rows, T, N, K)
+    _check(_lib.moe_grouped_matmul(ptr(x), ldx, x_rows, ptr(w), ldw, expert, _ref(g), T, N, K, ptr(y), y_dtype, ldy,
+                                   ptr(ws), ws_bytes, stream_handle(stream)), "moe_grouped_matmul")
+
+
+def moe_mx_grouped_matmul_workspace_bytes(x: moe_mx_rows, x_rows: int, w: moe_mx_rows, g: moe_groups, T: int, N: int,
+                                          B: int) -> int:
+    _sizes("moe_mx_grouped_matmul_workspace_bytes", x_rows, T, N, B)
+    return _lib.moe_mx_grouped_matmul_workspace_bytes(_ref(x), x_rows, _ref(w), _ref(g), T, N, B)
+
+
+def moe_mx_grouped_matmul(x: moe_mx_rows, x_rows: int, w: moe_mx_rows, g: moe_groups, T: int, N: int, B: int, y,
+                          y_dtype: int, ldy: int, ws, ws_bytes: int, stream=None) -> None:
+    _sizes("moe_mx_grouped_matmul", x_rows, T, N, B)
+    _check(_lib.moe_mx_grouped_matmul(_ref(x), x_rows, _ref(w), _ref(g), T, N, B, ptr(y), y_dtype, ldy, ptr(ws), ws_bytes,
+                                      stream_handle(stream)), "moe_mx_grouped_matmul")
+
+
+def moe_combine(z, z_dtype: int, ldz: int, T: int, w, place, S: int, k: int, H: int, add, lda: int, y, y_dtype: int,
+                ldy: int, stream=None) -> None:
+    _sizes("moe_combine", T, S, k, H)
+    _check(_lib.moe_combine(ptr(z), z_dtype, ldz, T, ptr(w), ptr(place), S, k, H, ptr(add), lda, ptr(y), y_dtype, ldy,
+                            stream_handle(stream)), "moe_combine")
+
+
+_MX_ROWS = struct.Struct("@PPqqqq")  # moe_mx_rows and moe_groups as bytes, as for rope
+_GROUPS = struct.Struct("@PPii")
+assert _MX_ROWS.size == ctypes.sizeof(moe_mx_rows) and _GROUPS.size == ctypes.sizeof(moe_groups)
+
+
+def _codes(q, e, what: str):
+    """(rows, blocks, row strides of q and e) of microscaled rows q [S, 16 B], e [S, B]."""
+    if q.dtype != torch.uint8 or e.dtype != torch.uint8:
+        raise ValueError(f"{what} and its scales must be uint8, not {q.dtype} and {e.dtype}")
+    if e.dim() != 2:
+        raise ValueError(f"{what}'s scales must be a matrix, not {tuple(e.shape)}")
+    S, B = e.shape
+    return S, B, _rows(q, (S, 16 * B), what), _rows(e, (S, B), f"{what}'s scales")
+
+
+def _matrices(t, shape, what: str):
+    """(row stride, matrix stride) of the matrices t [E, N, K], whose rows must be contiguous."""
+    if t.shape == shape and len(shape) == 3:
+        E, N, K = shape
+        if t.is_contiguous():
+            return K, N * K
+        a, b, c = t.stride()
+        if c == 1 or K <= 1:
+            return b if N > 1 else K, a if E > 1 else 0
+    raise ValueError(f"{what} must be [experts, rows, width] with contiguous rows, of shape {tuple(shape)}, not "
+                     f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+
+
+def _workspace_of(ws, need: int, like):
+    """(tensor, address, bytes) of the workspace given, or of a new one of `need` bytes."""
+    if ws is None:
+        if need <= 0:
+            return None, None, 0
+        ws = like.new_empty(need, dtype=torch.uint8)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _contiguous_ws(ws) -> None:
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, not of strides {tuple(ws.stride())}")
+
+
+def mx_quant(x, round_up: bool = False, stream=None):
+    """(q [S, 16 B], e [S, B]) uint8 of the rows x [S, H], B = ceil(H / 32): moe_mx_quant with its outputs allocated on
+    x's GPU.  round_up: MOE_MX_UP, scales under which no value is cut off."""
+    xd, shape = _code(x.dtype, "x"), x.shape
+    ldx = _rows(x, shape, "x")
+    S, H = shape
+    if (S | H) >> 31:
+        _sizes("moe_mx_quant", S, H)
+    gpu = _gpu(x)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, mx_quant, (x,), x, round_up)
+    B = (H + 31) // 32
+    q, e = x.new_empty((S, 16 * B), dtype=torch.uint8), x.new_empty((S, B), dtype=torch.uint8)
+    rc = _lib.moe_mx_quant(x.data_ptr(), xd, ldx, S, H, MOE_MX_UP if round_up else MOE_MX_FLOOR, q.data_ptr(), 16 * B,
+                           e.data_ptr(), B, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_mx_quant")
+    return q, e
+
+
+def mx_silu_quant(g, u=None, round_up: bool = False, stream=None):
+    """(q [S, 16 B], e [S, B]) of silu(g) * u, both [S, I], or of the halves of g [S, 2 I] where u is None:
+    moe_mx_silu_quant with its outputs allocated on g's GPU."""
+    xd, shape = _code(g.dtype, "g"), g.shape
+    ldx = _rows(g, shape, "g")
+    S, I = shape
+    up = g.data_ptr()
+    if u is None:
+        if I % 2:
+            raise ValueError(f"g holds gate and up side by side: its width {I} must be even")
+        I //= 2
+        up += I * g.element_size()
+    else:
+        if u.dtype != g.dtype:
+            raise ValueError(f"u must have g's type {g.dtype}, not {u.dtype}")
+        if _rows(u, shape, "u") != ldx:
+            raise ValueError(f"u must have g's row stride {ldx}, not {u.stride(0)}")
+        up = u.data_ptr()
+    if (S | I) >> 31:
+        _sizes("moe_mx_silu_quant", S, I)
+    gpu = _gpu(g, u)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, mx_silu_quant, (g, u), g, u, round_up)
+    B = (I + 31) // 32
+    q, e = g.new_empty((S, 16 * B), dtype=torch.uint8), g.new_empty((S, B), dtype=torch.uint8)
+    rc = _lib.moe_mx_silu_quant(g.data_ptr(), up, xd, ldx, S, I, MOE_MX_UP if round_up else MOE_MX_FLOOR, q.data_ptr(),
+                                16 * B, e.data_ptr(), B, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_mx_silu_quant")
+    return q, e
+
+
+def mx_values(q, e, width: int | None = None, dtype=None, stream=None):
+    """The numbers [S, width] (32 B unless given) that the microscaled rows q, e stand for, in dtype (bfloat16 unless
+    given): moe_mx_values with its output allocated on q's GPU."""
+    S, B, ldq, lde = _codes(q, e, "q")
+    dtype = dtype or torch.bfloat16
+    yd = _code(dtype, "dtype")
+    H = 32 * B if width is None else width
+    if not 32 * (B - 1) < H <= 32 * B:
+        raise ValueError(f"rows of {B} blocks hold {32 * (B - 1) + 1} to {32 * B} values, not {H}")
+    if (S | H) >> 31:
+        _sizes("moe_mx_values", S, H)
+    gpu = _gpu(q, e)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, mx_values, (q, e), q, e, width, dtype)
+    y = q.new_empty((S, H), dtype=dtype)
+    rc = _lib.moe_mx_values(q.data_ptr(), ldq, e.data_ptr(), lde, S, H, y.data_ptr(), yd, H, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_mx_values")
+    return y
+
+
+def mx_matmul(q, e, w, ew, out_dtype=None, ws=None, stream=None):
+    """y [S, N] in out_dtype (bfloat16 unless given): moe_mx_matmul of the microscaled rows q [S, 16 B], e [S, B] with the
+    microscaled weights w [N, 16 B], ew [N, B], with its output (and, when ws is None, a workspace) allocated on q's
+    GPU."""
+    out_dtype = out_dtype or torch.bfloat16
+    yd = _code(out_dtype, "out_dtype")
+    S, B, ldq, lde = _codes(q, e, "q")
+    N, Bw, ldw, ldew = _codes(w, ew, "w")
+    if Bw != B:
+        raise ValueError(f"q has rows of {B} blocks, w of {Bw}")
+    _contiguous_ws(ws)
+    if (S | N | B) >> 31:
+        _sizes("moe_mx_matmul", S, N, B)
+    gpu = _gpu(q, e, w, ew, ws)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, mx_matmul, (q, e, w, ew, ws), q, e, w, ew, out_dtype, ws)
+    px = _MX_ROWS.pack(q.data_ptr(), e.data_ptr(), ldq, lde, 0, 0)
+    pw = _MX_ROWS.pack(w.data_ptr(), ew.data_ptr(), ldw, ldew, 0, 0)
+    ws, pws, nws = _workspace_of(ws, _lib.moe_mx_matmul_workspace_bytes(px, pw, S, N, B), q)
+    y = q.new_empty((S, N), dtype=out_dtype)
+    rc = _lib.moe_mx_matmul(px, pw, S, N, B, y.data_ptr(), yd, N, pws, nws, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_mx_matmul")
+    return y
+
+
+def group(idx, n_experts: int, ws=None, stream=None):
+    """(first [n_experts + 1], order [S k], place [S, k]) int32 of a routing idx [S, k] int32: moe_group with its outputs
+    (and, when ws is None, a workspace) allocated on idx's GPU."""
+    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous():
+        raise ValueError(f"idx must be a contiguous int32 matrix, not {tuple(idx.shape)} {idx.dtype}")
+    S, k = idx.shape
+    _contiguous_ws(ws)
+    if (S | k | n_experts) >> 31:
+        _sizes("moe_group", S, k, n_experts)
+    gpu = _gpu(idx, ws)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, group, (idx, ws), idx, n_experts, ws)
+    ws, pws, nws = _workspace_of(ws, _lib.moe_group_workspace_bytes(S, k, n_experts), idx)
+    first, order, place = idx.new_empty(max(n_experts, 0) + 1), idx.new_empty(S * k), _empty_like(idx)
+    rc = _lib.moe_group(idx.data_ptr(), S, k, n_experts, first.data_ptr(), order.data_ptr(), place.data_ptr(), pws, nws,
+                        _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_group")
+    return first, order, place
+
+
+def _groups(first, order, top_k, E: int, x_rows: int):
+    """(rows of the product, moe_groups as bytes)."""
+    _vector(first, E + 1, torch.int32, "first")
+    if order is None:
+        if top_k is not None:
+            raise ValueError("top_k goes with order: none is given")
+        return x_rows, _GROUPS.pack(first.data_ptr(), 0, E, 0)
+    if top_k is None or not 0 < top_k <= 0x7FFFFFFF:
+        raise ValueError(f"order goes with top_k, the choices of a token, not {top_k}")
+    T = order.shape[0] if order.dim() == 1 else -1
+    _vector(order, T, torch.int32, "order")
+    return T, _GROUPS.pack(first.data_ptr(), order.data_ptr(), E, top_k)
+
+
+def _grouped_out(out, T: int, N: int, out_dtype, like):
+    """(output, its row stride, its dtype code)."""
+    if out is None:
+        out = like.new_empty((T, N), dtype=out_dtype or torch.bfloat16)
+        return out, N, _code(out.dtype, "out_dtype")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be of out_dtype {out_dtype}, not {out.dtype}")
+    return out, _rows(out, (T, N), "out"), _code(out.dtype, "out")
+
+
+def grouped_matmul(x, w, first, order=None, top_k: int | None = None, out_dtype=None, out=None, ws=None, stream=None):
+    """y [T, N] in out_dtype (bfloat16 unless given): moe_grouped_matmul of bf16 rows with the bf16 weights w [E, N, K] of
+    their experts, expert e's being rows first[e] .. first[e + 1] - 1 of y.  Row i's input is row i of x [T, K], or, where
+    order [T] is given, row order[i] // top_k of x.  The output (unless `out` is given) and a workspace (when ws is None)
+    are allocated on x's GPU; rows that no expert has are left as they were (of a new output: not initialised)."""
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise ValueError(f"x and w must be bfloat16, not {x.dtype} and {w.dtype}")
+    shape = x.shape
+    ldx = _rows(x, shape, "x")
+    rows, K = shape
+    E, N = w.shape[:2] if w.dim() == 3 else (0, 0)
+    ldw, expert = _matrices(w, (E, N, K), "w")
+    T, plan = _groups(first, order, top_k, E, rows)
+    _contiguous_ws(ws)
+    if (rows | T | N | K) >> 31:
+        _sizes("moe_grouped_matmul", rows, T, N, K)
+    if out_dtype is not None:
+        _code(out_dtype, "out_dtype")
+    gpu = _gpu(x, w, first, order, out, ws)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, grouped_matmul, (x, w, first, order, out, ws), x, w, first, order, top_k, out_dtype,
+                          out, ws)
+    over = out
+    out, ldy, yd = _grouped_out(out, T, N, out_dtype, x)
+    px, pw = x.data_ptr(), w.data_ptr()
+    ws, pws, nws = _workspace_of(ws, _lib.moe_grouped_matmul_workspace_bytes(px, ldx, rows, pw, ldw, expert, plan, T, N, K), x)
+    rc = _lib.moe_grouped_matmul(px, ldx, rows, pw, ldw, expert, plan, T, N, K, out.data_ptr(), yd, ldy, pws, nws,
+                                 _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_grouped_matmul")
+    if over is not None:
+        _written(over)
+    return out
+
+
+def mx_grouped_matmul(q, e, w, ew, first, order=None, top_k: int | None = None, out_dtype=None, out=None, ws=None,
+                      stream=None):
+    """y [T, N]: grouped_matmul of microscaled rows q [T, 16 B], e [T, B] with microscaled weights w [E, N, 16 B],
+    ew [E, N, B] (moe_mx_grouped_matmul)."""
+    rows, B, ldq, lde = _codes(q, e, "q")
+    if w.dtype != torch.uint8 or ew.dtype != torch.uint8:
+        raise ValueError(f"w and its scales must be uint8, not {w.dtype} and {ew.dtype}")
+    E, N = w.shape[:2] if w.dim() == 3 else (0, 0)
+    ldw, expert = _matrices(w, (E, N, 16 * B), "w")
+    ldew, expert_e = _matrices(ew, (E, N, B), "w's scales")
+    T, plan = _groups(first, order, top_k, E, rows)
+    _contiguous_ws(ws)
+    if (rows | T | N | B) >> 31:
+        _sizes("moe_mx_grouped_matmul", rows, T, N, B)
+    if out_dtype is not None:
+        _code(out_dtype, "out_dtype")
+    gpu = _gpu(q, e, w, ew, first, order, out, ws)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, mx_grouped_matmul, (q, e, w, ew, first, order, out, ws), q, e, w, ew, first, order,
+                          top_k, out_dtype, out, ws)
+    over = out
+    out, ldy, yd = _grouped_out(out, T, N, out_dtype, q)
+    px = _MX_ROWS.pack(q.data_ptr(), e.data_ptr(), ldq, lde, 0, 0)
+    pw = _MX_ROWS.pack(w.data_ptr(), ew.data_ptr(), ldw, ldew, expert, expert_e)
+    ws, pws, nws = _workspace_of(ws, _lib.moe_mx_grouped_matmul_workspace_bytes(px, rows, pw, plan, T, N, B), q)
+    rc = _lib.moe_mx_grouped_matmul(px, rows, pw, plan, T, N, B, out.data_ptr(), yd, ldy, pws, nws, _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_mx_grouped_matmul")
+    if over is not None:
+        _written(over)
+    return out
+
+
+def combine(z, w, place, add=None, out_dtype=None, stream=None):
+    """y [S, H] in out_dtype (z's type unless given), y[s] = sum_j w[s, j] z[place[s, j]] + add[s]: moe_combine of the
+    experts' rows z [T, H] with the weights w [S, k] fp32 and the places of group, with its output allocated on z's
+    GPU."""
+    zd, shape = _code(z.dtype, "z"), z.shape
+    ldz = _rows(z, shape, "z")
+    T, H = shape
+    if place.dim() != 2:
+        raise ValueError(f"place must be a matrix, not {tuple(place.shape)}")
+    pairs = place.shape
+    for name, t, dtype in (("place", place, torch.int32), ("w", w, torch.float32)):
+        if t.shape != pairs or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {tuple(pairs)} {dtype} tensor, not {tuple(t.shape)} {t.dtype}")
+    S, k = pairs
+    out_dtype = out_dtype or z.dtype
+    yd = _code(out_dtype, "out_dtype")
+    lda, pa = 0, None
+    if add is not None:
+        lda = _rows(add, (S, H), "add")
+        if add.dtype != z.dtype:
+            raise ValueError(f"add must have z's type {z.dtype}, not {add.dtype}")
+        pa = add.data_ptr()
+    if (T | S | k | H) >> 31:
+        _sizes("moe_combine", T, S, k, H)
+    gpu = _gpu(z, w, place, add)
+    if stream is not None or gpu != _current_gpu():
+        return _elsewhere(gpu, stream, combine, (z, w, place, add), z, w, place, add, out_dtype)
+    y = z.new_empty((S, H), dtype=out_dtype)
+    rc = _lib.moe_combine(z.data_ptr(), zd, ldz, T, w.data_ptr(), place.data_ptr(), S, k, H, pa, lda, y.data_ptr(), yd, H,
+                          _stream_of(gpu))
+    if rc:
+        raise MoeError(rc, "moe_combine")
+    return y
 
 
 def moe_profile_enable(on: bool) -> None:
