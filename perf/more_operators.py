@@ -176,7 +176,7 @@ def _plain_codes(v, up):
     e = torch.where(m > 0, (e + 127).clamp(0, 254), 0)
     a = v.abs().double() / _scales(e)
     c = torch.where(a < 2, (2 * a).round(), torch.where(a < 4, 2 + a.round(), 4 + (a / 2).round())).clamp(max=7).to(torch.uint8)
-    c = c + 8 * torch.signbit(v)
+    c = c + torch.signbit(v).to(torch.uint8) * 8
     return c[..., 0::2] + 16 * c[..., 1::2], e.to(torch.uint8)
 
 
