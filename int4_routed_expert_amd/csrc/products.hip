@@ -77,10 +77,12 @@ struct Where {
   int col;
 };
 
-__device__ inline int tiles_in(const ProdArgs &a, int e, int rows, int &lo, int &hi) {
-  lo = min(max(ldg<int32_t>(a.first + e), 0), a.T);
-  hi = min(max(ldg<int32_t>(a.first + e + 1), 0), a.T);
-  return hi > lo ? (hi - lo + rows - 1) / rows : 0;
+struct Range {
+  int lo, hi;
+  __device__ int tiles(int rows) const { return hi > lo ? (hi - lo + rows - 1) / rows : 0; }
+};
+__device__ inline Range range_of(const ProdArgs &a, int e) {
+  return {min(max(ldg<int32_t>(a.first + e), 0), a.T), min(max(ldg<int32_t>(a.first + e + 1), 0), a.T)};
 }
 
 // Blocks go to the XCDs round-robin; each XCD gets a contiguous run of tiles, so that those in
@@ -91,10 +93,9 @@ __device__ inline bool locate(const ProdArgs &a, int block, int rows, int cols, 
   const int lane = threadIdx.x & 63, share = (a.E + 63) / 64;
   int total = (a.T + rows - 1) / rows, n = 0, scan = 0;
   if (a.first) {
-    int lo, hi;
     for (int i = 0; i < share; ++i) {
       const int e = lane * share + i;
-      if (e < a.E) n += tiles_in(a, e, rows, lo, hi);
+      if (e < a.E) n += range_of(a, e).tiles(rows);
     }
     scan = n;
 #pragma unroll
@@ -112,15 +113,16 @@ __device__ inline bool locate(const ProdArgs &a, int block, int rows, int cols, 
     const int want = t / cols;
     const int at = 63 - __builtin_clzll(__ballot(scan - n <= want));  // the last lane that starts at or ahead of it
     before = __builtin_amdgcn_readlane(scan - n, at);
-    int e = at * share, lo, hi;
-    for (;; ++e) {  // ends: the lane's experts hold the tile
-      w.tiles = __builtin_amdgcn_readfirstlane(tiles_in(a, e, rows, lo, hi));
-      if (want < before + w.tiles || e + 1 >= a.E) break;
-      before += w.tiles;
+    int e = at * share;
+    Range r = range_of(a, e);
+    while (want >= before + r.tiles(rows) && e + 1 < a.E) {  // ends: the lane's experts hold the tile
+      before += r.tiles(rows);
+      r = range_of(a, ++e);
     }
     w.expert = e;
-    w.lo = __builtin_amdgcn_readfirstlane(lo);
-    w.hi = __builtin_amdgcn_readfirstlane(hi);
+    w.lo = __builtin_amdgcn_readfirstlane(r.lo);
+    w.hi = __builtin_amdgcn_readfirstlane(r.hi);
+    w.tiles = r.tiles(rows);
   } else {
     w.expert = 0; w.lo = 0; w.hi = a.T; w.tiles = total;
   }
@@ -373,6 +375,8 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
         if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
       const int k = m / kM, i = m % kM / TS, j = m % TS;
       acc[i][j] = mfma32<KIND>(F[cur][k][i], F[cur][k][TN + j], S[sn][i], S[sn][TN + j], now * kG + k, acc[i][j]);
+      // the compiler moves scaled products together, past the barrier below: 256 x 256 tiles spill then
+      if constexpr (kMicro) asm volatile("" : "+a"(acc[i][j]));
       __builtin_amdgcn_sched_barrier(0);
     }
   };
