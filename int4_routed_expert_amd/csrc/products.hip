@@ -68,70 +68,83 @@ __device__ inline int scale_at(const uint8_t *row, int k, int row_bytes) {
 }
 
 // ---- where a tile lies --------------------------------------------------------------------
-// Tiles of `rows` rows never cross experts.  They are counted on the GPU, by each wave for
-// itself: a lane adds up the tiles of its share of the experts, a scan over the lanes finds the
-// block's expert (there are `cols` column tiles for each row tile).
+// Tiles of `rows` rows that never cross experts, `cols` of them side by side for each.  They are
+// counted on the GPU, by each wave for itself: a lane adds up the row tiles of its share of the
+// experts, and a scan over the lanes says where that share begins.
 struct Where {
   int expert, lo, hi;  // its rows
-  int tile, tiles;     // the row tile within the expert, of how many (> 0)
-  int col;
+  int tile, col;       // the row tile within the expert, the column tile
 };
 
 struct Range {
   int lo, hi;
   __device__ int tiles(int rows) const { return hi > lo ? (hi - lo + rows - 1) / rows : 0; }
 };
-__device__ inline Range range_of(const ProdArgs &a, int e) {
-  return {min(max(ldg<int32_t>(a.first + e), 0), a.T), min(max(ldg<int32_t>(a.first + e + 1), 0), a.T)};
+template <class T>
+__device__ inline T ldk(const T *p) {  // of a wave-uniform address, through the scalar cache: no kernel here writes there
+  return *(const __attribute__((address_space(4))) T *)p;
 }
 
 // Blocks go to the XCDs round-robin; each XCD gets a contiguous run of tiles, so that those in
 // flight on it share weights, and within an expert rows, in its L2.  An expert's tiles go in strips of
-// kStrip row tiles, column by column.  False where there is no tile for the block.
+// kStrip row tiles, column by column.
 constexpr int kStrip = 4;
-__device__ inline bool locate(const ProdArgs &a, int block, int rows, int cols, Where &w) {
-  const int lane = threadIdx.x & 63, share = (a.E + 63) / 64;
-  int total = (a.T + rows - 1) / rows, n = 0, scan = 0;
-  if (a.first) {
-    for (int i = 0; i < share; ++i) {
-      const int e = lane * share + i;
-      if (e < a.E) n += range_of(a, e).tiles(rows);
-    }
-    scan = n;
+struct Tiles {
+  int rows, cols, share;
+  int n, from;  // this lane's row tiles, and those ahead of them
+  int per;      // tiles of an XCD
+  int total;
+  __device__ inline __attribute__((always_inline)) Tiles(const ProdArgs &a, int rows, int cols) : rows(rows), cols(cols), share((a.E + 63) / 64), n(0), from(0) {
+    if (a.first) {
+      const int lane = threadIdx.x & 63;
+      for (int i = 0; i < share; ++i) {
+        const int e = lane * share + i;
+        if (e < a.E) n += Range{bound(a, ldg<int32_t>(a.first + e)), bound(a, ldg<int32_t>(a.first + e + 1))}.tiles(rows);
+      }
+      from = n;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(scan, o);
-      if (lane >= o) scan += up;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(from, o);
+        if (lane >= o) from += up;
+      }
+      total = __builtin_amdgcn_readlane(from, 63) * cols;
+      from -= n;
+    } else {
+      total = (a.T + rows - 1) / rows * cols;
     }
-    total = __builtin_amdgcn_readlane(scan, 63);
+    per = (total + kXcds - 1) / kXcds;
   }
-  const int per = (total * cols + kXcds - 1) / kXcds;
-  const int t = block % kXcds * per + block / kXcds;
-  if (block / kXcds >= per || t >= total * cols) return false;
-  int before = 0;  // row tiles of the experts ahead
-  if (a.first) {
-    const int want = t / cols;
-    const int at = 63 - __builtin_clzll(__ballot(scan - n <= want));  // the last lane that starts at or ahead of it
-    before = __builtin_amdgcn_readlane(scan - n, at);
-    int e = at * share;
-    Range r = range_of(a, e);
-    while (want >= before + r.tiles(rows) && e + 1 < a.E) {  // ends: the lane's experts hold the tile
-      before += r.tiles(rows);
-      r = range_of(a, ++e);
+  __device__ static int bound(const ProdArgs &a, int i) { return min(max(i, 0), a.T); }
+
+  // Tile i of XCD x; false where there is none.
+  __device__ inline __attribute__((always_inline)) bool find(const ProdArgs &a, int x, int i, Where &w) const {
+    const int t = x * per + i;
+    if (i >= per || t >= total) return false;
+    int before = 0, tiles;  // row tiles of the experts ahead, of this one
+    if (a.first) {
+      const int want = t / cols;
+      const int at = 63 - __builtin_clzll(__ballot(from <= want));  // the last lane that starts at or ahead of it
+      before = __builtin_amdgcn_readlane(from, at);
+      int e = at * share, lo = bound(a, ldk(a.first + e)), hi = bound(a, ldk(a.first + e + 1));
+      while (want >= before + Range{lo, hi}.tiles(rows) && e + 1 < a.E) {  // ends: the lane's experts hold the tile
+        before += Range{lo, hi}.tiles(rows);
+        ++e;
+        lo = hi;
+        hi = bound(a, ldk(a.first + e + 1));
+      }
+      w.expert = e; w.lo = lo; w.hi = hi;
+      tiles = Range{lo, hi}.tiles(rows);
+    } else {
+      w.expert = 0; w.lo = 0; w.hi = a.T;
+      tiles = total / cols;
     }
-    w.expert = e;
-    w.lo = __builtin_amdgcn_readfirstlane(r.lo);
-    w.hi = __builtin_amdgcn_readfirstlane(r.hi);
-    w.tiles = r.tiles(rows);
-  } else {
-    w.expert = 0; w.lo = 0; w.hi = a.T; w.tiles = total;
+    const int in = t - before * cols, strip = in / (kStrip * cols), left = in - strip * kStrip * cols;
+    const int g = min(kStrip, tiles - strip * kStrip);
+    w.tile = strip * kStrip + left % g;
+    w.col = left / g;
+    return true;
   }
-  const int in = t - before * cols, strip = in / (kStrip * cols), left = in - strip * kStrip * cols;
-  const int g = min(kStrip, w.tiles - strip * kStrip);
-  w.tile = strip * kStrip + left % g;
-  w.col = left / g;
-  return true;
-}
+};
 
 // The row of x that row i of y is computed from, -1 where there is none.
 __device__ inline int source_of(const ProdArgs &a, int i) {
@@ -172,14 +185,34 @@ __device__ inline void store4(const ProdArgs &a, int64_t i, int n, f32x4 v) {
   }
 }
 
+// 16 bytes of outputs y[i, n ..] from LDS, those below N: eight bf16 or four fp32.
+template <bool BF16>
+__device__ inline void store16(const ProdArgs &a, int64_t i, int n, const uint8_t *from) {
+  constexpr int kEach = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;
+  typedef std::conditional_t<BF16, u32x4_h, u32x4_w> any;  // at any element
+  char *to = (char *)a.y + (i * a.ldy + n) * kSize;
+  if (n + kEach <= a.N) {
+    const u32x4_t v = *(const u32x4_t *)from;
+    if (a.stream) put(to, v, true);
+    else *(__attribute__((address_space(1))) any *)to = v;
+  } else {
+#pragma unroll 1
+    for (int j = 0; n + j < a.N; ++j) {
+      if constexpr (BF16) stg<uint16_t>(to + 2 * j, *(const uint16_t *)(from + 2 * j));
+      else stg<uint32_t>(to + 4 * j, *(const uint32_t *)(from + 4 * j));
+    }
+  }
+}
+
 // ---- straight from memory -----------------------------------------------------------------
 // A workgroup takes 16 weight rows and 16 NT rows of one expert; its W waves share out the row's
 // steps of 64 bytes and add their sums in LDS in a fixed order.
 template <Kind KIND, int NT, int W>
 __global__ __launch_bounds__(64 * W) void k_product_few(ProdArgs a, int cols) {
   __shared__ f32x4 s_acc[W][NT][64];
+  const Tiles tiles(a, 16 * NT, cols);
   Where at;
-  if (!locate(a, blockIdx.x, 16 * NT, cols, at)) return;
+  if (!tiles.find(a, blockIdx.x % kXcds, blockIdx.x / kXcds, at)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = at.col * 16, i0 = at.lo + at.tile * 16 * NT;
   const int row = lane & 15, kq = (lane >> 4) * 16;
@@ -225,217 +258,356 @@ __global__ __launch_bounds__(64 * W) void k_product_few(ProdArgs a, int cols) {
 }
 
 // ---- through LDS ----------------------------------------------------------------------------
-// A workgroup takes BN weight rows x BS rows of one expert, its WN x WS waves each their part in
-// blocks of 32 x 32; both operands go through LDS in stages of kBK bytes of K, NBUF of them, as in
-// the int8 product (qmatmul.hip, where the pipeline is described: 16 bytes a lane and 32 cycles an
-// instruction are the same).  Microscaled rows add a byte a block: 16 of a row, two stages'
-// worth, are one load into LDS, and a lane reads the four of its blocks of a stage as one word, of
-// which each instruction takes one byte.  For that a lane's blocks are neighbours: lanes 0 .. 31
-// take blocks 0 .. 3 of a stage's eight, lanes 32 .. 63 blocks 4 .. 7, in both operands.
+// A workgroup takes tiles of BN weight rows x BS rows of one expert, one after another; its WN x WS
+// waves have blocks of 32 x 32 of it, both operands go through LDS in stages of kBK bytes of K, NBUF
+// of them, and a stage's buffer is requested anew as soon as it has been read (as in the int8 product
+// of qmatmul.hip: 16 bytes a lane and 32 cycles an instruction are the same).
+//
+// The stages of a workgroup's tiles are one stream: while a tile's last stages are multiplied, the
+// first ones of the next tile are on their way, and its outputs leave while they arrive.  (A tile's
+// start and end by themselves took 12 us of 8192 x 12288 x 6144's 54 a tile.)
+//
+// An expert's last tile has fewer rows: a wave multiplies only the blocks that have some, which lie in
+// turn with the waves beside it (NS of them, 1 .. TS).
+//
+// Microscaled rows add a byte a block: 16 of a row, two stages' worth, are one load into LDS, and a
+// lane reads the four of its blocks of a stage as one word, of which each instruction takes one byte.
+// For that a lane's blocks are neighbours: lanes 0 .. 31 take blocks 0 .. 3 of a stage's eight, lanes 32
+// .. 63 blocks 4 .. 7, in both operands.
+// One 16-byte load from base + at straight into LDS, to lds + off + 16 lane (base and lds wave-uniform,
+// off a constant), by the lanes of `lanes`; it is issued, and counted, whichever they are.  All of the
+// wave's lanes are active where it stands.
+__device__ inline __attribute__((always_inline)) void load_to_lds(uint64_t lanes, const uint8_t *base, uint32_t at, uint32_t lds, int off) {
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+               ::"s"(lds), "v"(at), "s"(base), "i"(off), "s"(lanes) : "memory", "m0", "scc", "exec");
+}
+
+// v, of which the compiler no longer knows what it was: what is derived from it is derived here, and
+// takes no registers elsewhere.
+__device__ inline int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The kernel's arguments, loaded again: those that only a tile's start and end need take no registers
+// between them.
+__device__ inline __attribute__((always_inline)) ProdArgs args_anew() {
+  auto p = (const __attribute__((address_space(4))) ProdArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ProdArgs *)p;
+}
+
 constexpr int kScBlocks = 16;  // scales of a row that are loaded at once
 
-template <Kind KIND, int BN, int BS, int WN, int WS, int NBUF>
+template <Kind KIND, int BN, int BS, int WN, int WS, int NBUF, int TOGETHER>
 __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int cols) {
-  constexpr int kThr = 64 * WN * WS;
+  constexpr int kWaves = WN * WS, kThr = 64 * kWaves;
   constexpr int TN = BN / WN / 32, TS = BS / WS / 32;  // 32x32 blocks of a wave
   constexpr int kRows = BN + BS, kStage = kRows * kBK;
   constexpr int kPer = kStage / 16 / kThr;  // chunks a thread moves per stage
-  static_assert(kStage % (16 * kThr) == 0 && NBUF % 2 == 0, "stage split");
+  static_assert(kStage % (16 * kThr) == 0, "stage split");
   constexpr bool kMicro = KIND == kMx;
   constexpr int kSc = kMicro ? (kRows + kThr - 1) / kThr : 0;  // scale loads of a thread per two stages
-  constexpr int kScSize = kSc * kThr * kScBlocks;
-  constexpr int kWide = BN / WN, kLd = kWide + 4;  // a wave's weights, and what a row's sums of them take in LDS
-  constexpr int kTurn = WN * WS * 32 * kLd * 4, kEnd = kTurn + BS * 4;
-  constexpr int kLds = std::max(NBUF * kStage + NBUF * kScSize, kEnd);
-  __shared__ __align__(128) uint8_t s_buf[kLds];
-  Where at;
-  if (!locate(a, blockIdx.x, BS, cols, at)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kScSize = kMicro ? kRows * kScBlocks : 0;
+  // Buffers of scales: one in use and those on their way.  Of four stages the readers of a pair's second
+  // scales have not met again when the pair two further on is requested.
+  constexpr int kScBufs = NBUF <= 3 ? 2 : 4;
+  constexpr int kScAt = NBUF * kStage, kOutAt = kScAt + kScBufs * kScSize;
+  // A wave turns 32 rows of kLine bytes of outputs round at once: whole cache lines, or half ones where
+  // that lets two workgroups share a compute unit.
+  constexpr int kLine = TOGETHER == 1 || TOGETHER * (kOutAt + kWaves * 32 * 128) <= 160 * 1024 ? 128 : 64;
+  constexpr int kOut = 32 * kLine;
+  static_assert(TOGETHER * (kOutAt + kWaves * kOut) <= 160 * 1024, "LDS");
+  __shared__ __align__(128) uint8_t s_buf[kOutAt + kWaves * kOut];
+  const Tiles tiles(a, BS, cols);
+  const int xcd = blockIdx.x % kXcds, apart = gridDim.x / kXcds;
+  int turn = blockIdx.x / kXcds;
+  Where at, next;
+  if (!tiles.find(a, xcd, turn, at)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave / WS, wsv = wave % WS;
-  const int n0 = at.col * BN, i0 = at.lo + at.tile * BS;
-
-  // row r of the tile: of the weights, or of x
-  auto row_of = [&](int r) __attribute__((always_inline)) {
-    return r < BN ? min(n0 + r, a.N - 1) : max(source_of(a, min(i0 + r - BN, at.hi - 1)), 0);
-  };
-  // this thread's chunks of a stage: LDS position tid + i kThr, which holds chunk c of row r
-  const uint8_t *src[kPer], *sc[kSc + 1];
-  int kc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    constexpr int kC = kBK / 16;
-    const int p = tid + i * kThr, r = p / kC;
-    kc[i] = ((p % kC) ^ mix_of(r)) << 4;
-    src[i] = (r < BN ? a.w + at.expert * a.expert + row_of(r) * a.ldw : a.x + row_of(r) * a.ldx) + kc[i];
-  }
-#pragma unroll
-  for (int i = 0; i < kSc; ++i) {
-    const int r = min(tid + i * kThr, kRows - 1);
-    sc[i] = r < BN ? a.we + at.expert * a.expert_e + row_of(r) * a.ldwe : a.xe + row_of(r) * a.ldxe;
-  }
-  const int stages = (a.row_bytes + kBK - 1) / kBK, whole = a.row_bytes / kBK;
-  const int sc_bytes = a.row_bytes / 16;
-
-  f32x16 acc[TN][TS];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TS; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-
   const int row = lane & 31, ck = lane >> 5;
-  constexpr int kSteps = kBK / 32;
-  int at_w[kSteps], at_x[kSteps];
+
+  // This thread's chunks of a stage: LDS position tid + i kThr, which holds chunk c of row r of the
+  // tile, the weights' rows first.  (kThr / 8 rows further on chunks are mixed alike.)
+  constexpr int kC = kBK / 16;
+  static_assert(kThr / kC % 16 == 0, "chunks are mixed over 16 rows");
+  const int kc = ((tid % kC) ^ mix_of(tid / kC)) << 4;
+  constexpr int kApart = kThr / kC;  // rows from one chunk of a thread to the next
+  static_assert(BN % kApart == 0, "a load has rows of one operand");
+  // A tile's operands by a base each (that of x its first row, or with order the whole of it) and a
+  // 32-bit offset a chunk; the base goes on through K.
+  const uint8_t *w_at, *x_at, *we_at, *xe_at;
+  uint32_t src[kPer], sc[kSc + 1];
+  uint32_t bad = 0, bad_next = 0;  // bit j: this lane's row of block j has no input
+  auto set_up = [&](const Where &w, uint32_t &lost) __attribute__((always_inline)) {
+    const ProdArgs a = args_anew();
+    const int n0 = w.col * BN, i0 = w.lo + w.tile * BS, tid = anew(threadIdx.x), row = tid & 31;
+    const int x0 = a.order ? 0 : min(i0, a.x_rows - 1);
+    w_at = a.w + w.expert * a.expert + n0 * a.ldw;
+    x_at = a.x + x0 * a.ldx;
+    auto x_row = [&](int r) __attribute__((always_inline)) { return source_of(a, min(i0 + r, w.hi - 1)); };
+    auto x_off = [&](int r) __attribute__((always_inline)) { return (uint32_t)max(x_row(r) - x0, 0); };
+    auto w_off = [&](int r) __attribute__((always_inline)) { return (uint32_t)min(r, a.N - 1 - n0); };
 #pragma unroll
-  for (int kk = 0; kk < kSteps; ++kk) {
-    at_w[kk] = chunk_of(wn * kWide + row, ck * kSteps + kk);
-    at_x[kk] = chunk_of(BN + wsv * (BS / WS) + row, ck * kSteps + kk);
-  }
-  constexpr int kF = TN + TS, kM = TN * TS;
-  auto frag = [&](const uint8_t *buf, int f, int kk) __attribute__((always_inline)) {
-    return *(const i32x4 *)(buf + (f < TN ? at_w[kk] + f * 32 * kBK : at_x[kk] + (f - TN) * 32 * kBK));
+    for (int i = 0; i < kPer; ++i) {
+      const int r = tid / kC + i * kApart;
+      src[i] = kc + (i * kApart < BN ? w_off(r) * (uint32_t)a.ldw : x_off(r - BN) * (uint32_t)a.ldx);
+    }
+    if constexpr (kMicro) {
+      we_at = a.we + w.expert * a.expert_e + n0 * a.ldwe;
+      xe_at = a.xe + x0 * a.ldxe;
+#pragma unroll
+      for (int i = 0; i < kSc; ++i) {
+        // threads past the last row repeat their first load
+        const int r = tid + i * kThr < kRows ? tid + i * kThr : tid;
+        sc[i] = r < BN ? w_off(r) * (uint32_t)a.ldwe : x_off(r - BN) * (uint32_t)a.ldxe;
+      }
+    }
+    lost = 0;
+    if (a.order) {
+#pragma unroll
+      for (int j = 0; j < TS; ++j) lost |= (x_row((wsv + WS * j) * 32 + row) < 0 ? 1u : 0u) << j;
+    }
   };
-  const uint8_t *s_sc = s_buf + NBUF * kStage;
-  const int sc_w = (wn * kWide + row) * kScBlocks + ck * 4, sc_x = (BN + wsv * (BS / WS) + row) * kScBlocks + ck * 4;
-  // the scales of fragment f in the stage whose scales lie at `from`
-  auto scale = [&](int f, int from) __attribute__((always_inline)) {
-    return *(const int *)(s_sc + from + (f < TN ? sc_w + f * 32 * kScBlocks : sc_x + (f - TN) * 32 * kScBlocks));
+  set_up(at, bad);
+  const int sc_bytes = a.row_bytes / 16;
+  // stages of a tile: an even number, so that scales come in pairs (beyond K they are zeros)
+  const int stages = max(((a.row_bytes + kBK - 1) / kBK + 1) & ~1, (NBUF + 1) & ~1);
+
+  constexpr int kSteps = kBK / 32;
+  // this lane's bytes of k step 0 in the wave's first blocks; those of step kk differ in bits 4 and 5
+  const int at_w = chunk_of(wn * (BN / WN) + row, ck * kSteps), at_x = chunk_of(BN + wsv * 32 + row, ck * kSteps);
+  // fragment f of a k step of the stage at `buf`: the wave's TN weight blocks, then its blocks of rows
+  auto frag = [&](int buf, int f, int kk) __attribute__((always_inline)) {
+    return *(const i32x4 *)(s_buf + (f < TN ? (at_w ^ kk << 4) + buf + f * 32 * kBK : (at_x ^ kk << 4) + buf + (f - TN) * 32 * WS * kBK));
+  };
+  const int sc_w = kScAt + (wn * (BN / WN) + row) * kScBlocks + ck * 4, sc_x = kScAt + (BN + wsv * 32 + row) * kScBlocks + ck * 4;
+  // its scales; those of the stage's pair lie at `pair`
+  auto scale = [&](int pair, int f) __attribute__((always_inline)) {
+    return *(const int *)(s_buf + pair + (f < TN ? sc_w + f * 32 * kScBlocks : sc_x + (f - TN) * 32 * WS * kScBlocks));
   };
 
   const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)s_buf + wave * 1024);
-  auto clip = [&](int s) __attribute__((always_inline)) {  // before stage s is requested
-    if (s >= whole) {
+  // Stage s of the tile that was set up last is requested next, into `buf`: `lanes` have bytes of its rows,
+  // the others write zeros themselves.
+  uint64_t lanes;
+  const uint8_t *w_k, *x_k;
+  auto aim = [&](int s, int buf) __attribute__((always_inline)) {
+    w_k = w_at + s * kBK;
+    x_k = x_at + s * kBK;
+    const bool in = s * kBK + kc < a.row_bytes;
+    lanes = __ballot(in);
+    if (!in) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if ((int64_t)s * kBK + kc[i] >= a.row_bytes) src[i] = g_zeros;
-    }
-    if constexpr (kMicro) {
-      if (s % 2 == 0 && s * 8 >= sc_bytes) {
-#pragma unroll
-        for (int i = 0; i < kSc; ++i) sc[i] = g_zeros;
-      }
+      for (int i = 0; i < kPer; ++i) *(u32x4_t *)(s_buf + buf + (tid + i * kThr) * 16) = u32x4_t{0, 0, 0, 0};
     }
   };
-  auto request = [&](int i, int buffer) __attribute__((always_inline)) {
-    load_to_lds((const int8_t *)src[i], lds, buffer * kStage + i * kThr * 16);
-    src[i] += kBK;
+  auto request = [&](int i, int buf) __attribute__((always_inline)) {
+    load_to_lds(lanes, i * kApart < BN ? w_k : x_k, src[i], lds + buf, i * kThr * 16);
   };
-  // The scales of stages s and s + 1 (s even), with the requests of stage s.  A buffer of scales is
-  // written again NBUF pairs of stages later, when its last readers have met twice.
-  auto request_scales = [&](int s) __attribute__((always_inline)) {
+  int sc_put = 0, sc_get = 0;  // the pair of scales to be requested next, and that in use
+  auto following = [](int at, int size, int n) __attribute__((always_inline)) { return at + size == n * size ? 0 : at + size; };
+  auto request_scales = [&](int s) __attribute__((always_inline)) {  // of stages s and s + 1 of a tile
     if constexpr (kMicro) {
+      const bool in = s * 8 < sc_bytes;
 #pragma unroll
       for (int i = 0; i < kSc; ++i) {
-        load_to_lds((const int8_t *)sc[i], lds + (s / 2 % NBUF) * kScSize, NBUF * kStage + i * kThr * 16);
-        sc[i] += kScBlocks;
+        const int r0 = wave * 64 + i * kThr < kRows ? i * kThr : 0;  // the wave's rows go from there
+        load_to_lds(__ballot(in), (wave * 64 + r0 < BN ? we_at : xe_at) + s * 8, sc[i], lds + sc_put + r0 * 16, kScAt);
+        if (!in) *(u32x4_t *)(s_buf + kScAt + sc_put + (tid + r0) * 16) = u32x4_t{0, 0, 0, 0};
       }
+      sc_put = following(sc_put, kScSize, kScBufs);
     }
   };
-  constexpr int kG = kM >= 8 ? 1 : kM >= 4 ? 2 : 4, kGroups = kSteps / kG;
+  // Requests in flight behind stage s + 1 when a stage s with s % 2 == U waits for it: stages s + 2 .. s +
+  // NBUF - 1, the even ones with scales.
+  constexpr auto kBehind = [](int u) {
+    int n = 0;
+    for (int k = 2; k < NBUF; ++k) n += kPer + ((u + k) % 2 == 0 ? kSc : 0);
+    return n;
+  };
+  constexpr int kFull = TN * TS;
+  constexpr int kG = kFull >= 8 ? 1 : kFull >= 4 ? 2 : 4, kGroups = kSteps / kG;  // k steps whose fragments are read at once
   constexpr int kSpread = kGroups > 1 ? 2 : 1;
-  // Requests in flight behind the stage that is waited for: the NBUF - 2 stages after it, half of which
-  // are even and bring scales.
-  constexpr int kBehind = (NBUF - 2) * kPer + (NBUF - 2) / 2 * kSc;
+  constexpr int kF = TN + TS;
 #pragma unroll
   for (int s = 0; s < NBUF; ++s) {
-    clip(s);
+    aim(s, s * kStage);
     if (s % 2 == 0) request_scales(s);
 #pragma unroll
-    for (int i = 0; i < (s < NBUF - 1 ? kPer : kPer / kSpread); ++i) request(i, s);
+    for (int i = 0; i < (s < NBUF - 1 ? kPer : kPer / kSpread); ++i) request(i, s * kStage);
   }
-  wait_and_meet<kBehind + kPer / kSpread>();
+  wait_and_meet<kBehind(1) + ((NBUF - 1) % 2 == 0 ? kSc : 0) + kPer / kSpread>();
   i32x4 F[2][kG][kF];
   int S[2][kF] = {};
+  int buf = 0, last = (NBUF - 1) * kStage;  // buffers of the current stage and of the one before it
+  int ask = NBUF - 1;                       // the stage requested last, of the tile that was set up last
+  auto read_first = [&](int f0) __attribute__((always_inline)) {  // of a tile's first group, fragments f0 ..
 #pragma unroll
-  for (int f = 0; f < kG * kF; ++f) F[0][f / kF][f % kF] = frag(s_buf, f % kF, f / kF);
-  if constexpr (kMicro) {
+    for (int k = 0; k < kG; ++k)
 #pragma unroll
-    for (int f = 0; f < kF; ++f) S[0][f] = scale(f, 0);
-  }
-  // Multiply group `now` of a stage (its fragments F[cur], its scales S[sn]) while the fragments of
-  // group g in `buffer` are read, and with g = 0 the next stage's scales, which lie at sc_from; buffer
-  // `again` is requested meanwhile.
-  auto multiply = [&](int cur, int sn, int now, int buffer, int g, int sc_from, int again, int r0, int r1)
-      __attribute__((always_inline)) {
-    constexpr int kAll = kG * kM;
+      for (int f = 0; f < kF; ++f)
+        if (f >= f0) F[0][k][f] = frag(buf, f, k);
+    if constexpr (kMicro) {
 #pragma unroll
-    for (int m = 0; m < kAll; ++m) {
-#pragma unroll
-      for (int f = 0; f < kG * kF; ++f)
-        if (f * kAll / (kG * kF) == m) F[cur ^ 1][f / kF][f % kF] = frag(s_buf + buffer * kStage, f % kF, g * kG + f / kF);
-      if constexpr (kMicro) {
-#pragma unroll
-        for (int f = 0; f < kF; ++f)
-          if (g == 0 && f * kAll / kF == m) S[sn ^ 1][f] = scale(f, sc_from);
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
-      const int k = m / kM, i = m % kM / TS, j = m % TS;
-      acc[i][j] = mfma32<KIND>(F[cur][k][i], F[cur][k][TN + j], S[sn][i], S[sn][TN + j], now * kG + k, acc[i][j]);
-      // the compiler moves scaled products together, past the barrier below: 256 x 256 tiles spill then
-      if constexpr (kMicro) asm volatile("" : "+a"(acc[i][j]));
-      __builtin_amdgcn_sched_barrier(0);
+      for (int f = 0; f < kF; ++f)
+        if (f >= f0) S[0][f] = scale(sc_get, f);
     }
   };
-  auto stage = [&](int s, int b) __attribute__((always_inline)) {  // stage s, in buffer b
-    const int cur = b * kGroups & 1, sn = b & 1;
-#pragma unroll
-    for (int g = 1; g < kGroups; ++g) {
-      multiply((cur + g - 1) & 1, sn, g - 1, b, g, 0, (b + NBUF - 1) % NBUF, g < kSpread ? kPer * g / kSpread : 0,
-               g < kSpread ? kPer * (g + 1) / kSpread : 0);
-    }
-    wait_and_meet<kBehind>();
-    clip(s + NBUF);
-    if (b % 2 == 0) request_scales(s + NBUF);
-    multiply((cur + kGroups - 1) & 1, sn, kGroups - 1, (b + 1) % NBUF, 0, ((s + 1) / 2 % NBUF) * kScSize + (b + 1) % 2 * 8, b, 0,
-             kPer / kSpread);
-  };
-  int s = 0;
-  for (; s + NBUF <= stages; s += NBUF) {
-#pragma unroll
-    for (int b = 0; b < NBUF; ++b) stage(s + b, b);
-  }
-#pragma unroll
-  for (int b = 0; b < NBUF - 1; ++b)
-    if (s + b < stages) stage(s + b, b);
-  wait_and_meet<0>();  // the last requests, beyond K, have arrived too
-  // Each wave turns its sums round in its own part of the buffers, 32 rows at a time, so that they
-  // leave as runs of a row's neighbouring outputs.
-  int *s_src = (int *)(s_buf + kTurn);
-  if (a.order) {
-    for (int i = tid; i < BS; i += kThr) s_src[i] = source_of(a, min(i0 + i, at.hi - 1));
-    __syncthreads();
-  }
-  float *out = (float *)s_buf + wave * 32 * kLd;
-  constexpr int kRun = kWide / 4, kTok = 64 / kRun;  // lanes of a row's run, rows at a time
-#pragma unroll
-  for (int j = 0; j < TS; ++j) {
+  read_first(0);
+
+  bool more = true;
+  auto tile = [&](auto blocks) __attribute__((always_inline)) {
+    constexpr int NS = decltype(blocks)::value, kM = TN * NS, kUse = TN + NS;
+    f32x16 acc[TN][NS];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *(f32x4 *)(out + row * kLd + i * 32 + 8 * e + 4 * ck) =
-            f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-    own_lds_done();
-    const int n = n0 + wn * kWide + (lane % kRun) * 4;
-    auto leave = [&](auto stream) __attribute__((always_inline)) {
-#pragma unroll 4
-      for (int r = lane / kRun; r < 32; r += kTok) {
-        const int sl = wsv * (BS / WS) + j * 32 + r;
-        f32x4 v = *(const f32x4 *)(out + r * kLd + (lane % kRun) * 4);
-        if (i0 + sl < at.hi && n < a.N) {
-          if (a.order && s_src[sl] < 0) v = nan4();
-          store4<decltype(stream)::value>(a, i0 + sl, n, v);
+      for (int j = 0; j < NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    // Multiply group `now` of a stage (its fragments F[cur], its scales S[sn]) while the fragments of
+    // group g of the stage at `from` are read, with g = 0 the next stage's scales too, and buffer
+    // `again` is requested.
+    auto multiply = [&](int cur, int sn, int now, int from, int g, int pair, int again, int r0, int r1)
+        __attribute__((always_inline)) {
+      constexpr int kAll = kG * kM;
+#pragma unroll
+      for (int m = 0; m < kAll; ++m) {
+#pragma unroll
+        for (int f = 0; f < kG * kUse; ++f)
+          if (f * kAll / (kG * kUse) == m) F[cur ^ 1][f / kUse][f % kUse] = frag(from, f % kUse, g * kG + f / kUse);
+        if constexpr (kMicro) {
+#pragma unroll
+          for (int f = 0; f < kUse; ++f)
+            if (g == 0 && f * kAll / kUse == m) S[sn ^ 1][f] = scale(pair, f);
         }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i >= r0 && i < r1 && (i - r0) * kAll / (r1 - r0) == m) request(i, again);
+        const int k = m / kM, i = m % kM / NS, j = m % NS;
+        acc[i][j] = mfma32<KIND>(F[cur][k][i], F[cur][k][TN + j], S[sn][i], S[sn][TN + j], now * kG + k, acc[i][j]);
+        // the compiler moves scaled products together, past the barrier below: 256 x 256 tiles spill then
+        if constexpr (kMicro) asm volatile("" : "+a"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    if (a.stream) leave(std::true_type());
+    auto stage = [&](auto odd) __attribute__((always_inline)) {  // a stage of the tile, an even or an odd one
+      constexpr int u = decltype(odd)::value, cur = u * kGroups & 1;
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g)
+        multiply((cur + g - 1) & 1, u, g - 1, buf, g, 0, last, g < kSpread ? kPer * g / kSpread : 0,
+                 g < kSpread ? kPer * (g + 1) / kSpread : 0);
+      wait_and_meet<kBehind(u)>();
+      if (++ask == stages) ask = 0;
+      if constexpr (u == NBUF % 2) {  // of these two stages the one that can ask for stage 0
+        if (ask == 0) {  // of the next tile (after the last one its own are loaded again, and not used)
+          turn += apart;
+          more = tiles.find(args_anew(), xcd, turn, next);
+          if (more) set_up(next, bad_next);
+        }
+      }
+      aim(ask, buf);
+      if ((u + NBUF) % 2 == 0) request_scales(ask);
+      const int then = following(buf, kStage, NBUF);
+      const int pair = u ? following(sc_get, kScSize, kScBufs) : sc_get + 8;
+      multiply((cur + kGroups - 1) & 1, u, kGroups - 1, then, 0, pair, buf, 0, kPer / kSpread);
+      if (u) sc_get = pair;
+      last = buf;
+      buf = then;
+    };
+#pragma unroll 1
+    for (int s = 0; s < stages; s += 2) {
+      stage(std::integral_constant<int, 0>());
+      stage(std::integral_constant<int, 1>());
+    }
+    // Each wave turns its sums round in LDS, kLine bytes of 32 rows at a time, so that they leave as whole
+    // cache lines.  A wave's accesses to LDS are carried out in order, so none waits for another.
+    const ProdArgs b = args_anew();
+    auto leave = [&](auto bf16) __attribute__((always_inline)) {
+      constexpr bool BF16 = decltype(bf16)::value;
+      constexpr int kI = BF16 && TN > 1 && kLine == 128 ? 2 : 1;  // blocks of weights at once
+      constexpr int kE = !BF16 && kLine == 64 ? 2 : 4;             // quarters of a block at once
+      constexpr int kSize = BF16 ? 2 : 4, kEach = 16 / kSize;      // outputs of a 16-byte piece
+      constexpr int kCh = kI * kE * 8 / kEach;                     // pieces of a row
+      constexpr int kQ = kCh / 2;                                  // rows, and pieces, of a lane
+      const int lane = anew(tid) & 63, row = lane & 31, ck = lane >> 5;
+      uint8_t *out = s_buf + kOutAt + wave * kOut;
+      auto piece = [&](int r, int c) __attribute__((always_inline)) { return out + r * kLine + ((c ^ (mix_of(r) & (kLine / 16 - 1))) << 4); };
+      const int i0 = at.lo + at.tile * BS, n0 = at.col * BN + wn * (BN / WN);
+      uint8_t *y = (uint8_t *)b.y + (i0 * b.ldy + n0) * kSize;
+      const int rows = at.hi - i0;
+      const bool whole = n0 + BN / WN <= b.N;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const bool lost = bad >> j & 1;
+        const float none = __builtin_nanf("");
+        const int r0 = (wsv + WS * j) * 32;
+#pragma unroll
+        for (int i = 0; i < TN; i += kI)
+#pragma unroll
+          for (int e0 = 0; e0 < 4; e0 += kE) {
+#pragma unroll
+            for (int h = 0; h < kI; ++h)
+#pragma unroll
+              for (int e = e0; e < e0 + kE; ++e) {
+                f32x4 v = {acc[i + h][j][4 * e], acc[i + h][j][4 * e + 1], acc[i + h][j][4 * e + 2], acc[i + h][j][4 * e + 3]};
+                if (lost) v = f32x4{none, none, none, none};
+                if constexpr (BF16)
+                  *(uint64_t *)(piece(row, h * 4 + e) + ck * 8) = ((uint64_t)pack2_bf16(v[2], v[3]) << 32) | pack2_bf16(v[0], v[1]);
+                else
+                  *(f32x4 *)piece(row, 2 * (e - e0) + ck) = v;
+              }
+            asm volatile("" ::: "memory");
+            const int n = i * 32 + e0 * 8;  // of the wave's outputs
+            if (whole) {
+              u32x4_t v[kQ];
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) v[q] = *(const u32x4_t *)piece(lane / kCh + q * (64 / kCh), lane % kCh);
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) {
+                typedef std::conditional_t<BF16, u32x4_h, u32x4_w> any;  // at any element
+                const int r = r0 + lane / kCh + q * (64 / kCh);
+                auto *to = (__attribute__((address_space(1))) any *)(y + n * kSize + (uint32_t)(r * (int)b.ldy + lane % kCh * kEach) * kSize);
+                if (r < rows) {
+                  if (b.stream) put<16>((void *)to, v[q], true);
+                  else *to = v[q];
+                }
+              }
+            } else {
+#pragma unroll 1
+              for (int r = lane / kCh; r < 32; r += 64 / kCh)
+                if (r0 + r < rows) store16<BF16>(b, i0 + r0 + r, n0 + n + lane % kCh * kEach, piece(r, lane % kCh));
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
+    };
+    if (b.y_bf16) leave(std::true_type());
     else leave(std::false_type());
-    own_lds_done();
-  }
+    if (NS < TS) read_first(kUse);
+  };
+  do {
+    const int blocks = (min(at.hi - at.lo - at.tile * BS, BS) + 32 * WS - 1) / (32 * WS);
+    if constexpr (TS == 1) {
+      tile(std::integral_constant<int, 1>());
+    } else if constexpr (TS == 2) {
+      if (blocks > 1) tile(std::integral_constant<int, 2>());
+      else tile(std::integral_constant<int, 1>());
+    } else {
+      static_assert(TS == 4, "blocks of a wave");
+      if (blocks > 3) tile(std::integral_constant<int, 4>());
+      else if (blocks > 2) tile(std::integral_constant<int, 3>());
+      else if (blocks > 1) tile(std::integral_constant<int, 2>());
+      else tile(std::integral_constant<int, 1>());
+    }
+    at = next;
+    bad = bad_next;
+  } while (more);
+  wait_and_meet<0>();  // the last requests, of zeros, have arrived
 }
 
 // ---- rows on 16-byte boundaries -------------------------------------------------------------
@@ -481,7 +653,10 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
   ProdPlan p{};
   const int busy = a.first ? std::min(a.E, a.T) : 1;
   const double rows = (double)a.T / busy;
+  // the tiles' offsets have 32 bits
+  const int64_t far = std::max({256 * a.ldw, 1024 * a.ldy, (a.order ? (int64_t)a.x_rows : 256) * a.ldx, 256 * a.ldwe, (a.order ? (int64_t)a.x_rows : 256) * a.ldxe});
   p.kernel = rows < 16 ? kFew16 : rows < 40 ? kFew32 : rows < 100 ? kTile64 : rows < 400 ? kTile128 : kTile256;
+  if (far >> 32) p.kernel = kFew32;
   if (p.kernel >= kTile64) {
     const int64_t row = mx ? a.row_bytes / 16 : a.row_bytes;
     const bool even = row % 16 == 0;
@@ -509,10 +684,11 @@ void launch_few(const ProdArgs &a, hipStream_t st) {
   const int cols = (a.N + 15) / 16;
   MOE_LAUNCH((k_product_few<KIND, NT, W>), dim3(blocks_of(a, 16 * NT, cols)), dim3(64 * W), 0, st, a, cols);
 }
-template <Kind KIND, int BN, int BS, int WN, int WS, int NBUF>
+template <Kind KIND, int BN, int BS, int WN, int WS, int NBUF, int TOGETHER>
 void launch_tile(const ProdArgs &a, hipStream_t st) {
   const int cols = (a.N + BN - 1) / BN;
-  MOE_LAUNCH((k_product_tile<KIND, BN, BS, WN, WS, NBUF>), dim3(blocks_of(a, BS, cols)), dim3(64 * WN * WS), 0, st, a, cols);
+  const unsigned most = 256 * TOGETHER;  // on the chip at once
+  MOE_LAUNCH((k_product_tile<KIND, BN, BS, WN, WS, NBUF, TOGETHER>), dim3(std::min(blocks_of(a, BS, cols), most)), dim3(64 * WN * WS), 0, st, a, cols);
 }
 
 template <Kind KIND>
@@ -520,9 +696,9 @@ void launch_piece(const ProdArgs &a, ProdKernel k, hipStream_t st) {
   switch (k) {
     case kFew16: launch_few<KIND, 1>(a, st); break;
     case kFew32: launch_few<KIND, 2>(a, st); break;
-    case kTile64: launch_tile<KIND, 128, 64, 2, 2, 4>(a, st); break;
-    case kTile128: launch_tile<KIND, 128, 128, 2, 2, 2>(a, st); break;
-    case kTile256: launch_tile<KIND, 256, 256, 2, 2, 2>(a, st); break;
+    case kTile64: launch_tile<KIND, 128, 64, 2, 2, 4, 1>(a, st); break;
+    case kTile128: launch_tile<KIND, 128, 128, 2, 2, 2, 2>(a, st); break;
+    case kTile256: launch_tile<KIND, 256, 256, 2, 2, 2, 1>(a, st); break;
   }
 }
 
@@ -549,7 +725,8 @@ hipError_t launch_product(const ProdArgs &a0, bool mx, hipStream_t st) {
   ProdArgs a = a0;
   const int ys = a.y_bf16 ? 2 : 4;
   a.y_vec = (uintptr_t)a.y % (a.y_bf16 ? 8 : 16) == 0 && a.ldy % 4 == 0;
-  a.stream = (int64_t)a.T * a.N * ys > kStreamBytes;
+  // past the caches only whole 16-byte pieces
+  a.stream = (int64_t)a.T * a.N * ys > kStreamBytes && (uintptr_t)a.y % 16 == 0 && a.ldy * ys % 16 == 0;
   const ProdPlan p = plan_of(a, mx);
   const int row = mx ? a.row_bytes / 16 : a.row_bytes;
   if (p.copy_x) {
