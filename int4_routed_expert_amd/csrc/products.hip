@@ -1,6 +1,7 @@
 // Products of rows with weights, dense or grouped by expert, both operands bf16 or microscaled:
 // y[i, n] = sum_k x[r(i), k] w[e(i), n, k], summed in fp32.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "experts.h"
@@ -161,19 +162,16 @@ __device__ inline f32x4 nan4() {
   return f32x4{n, n, n, n};
 }
 
-// Four neighbouring outputs y[i, n .. n + 3], those below N, past the caches where STREAM.
-template <bool STREAM>
+// Four neighbouring outputs y[i, n .. n + 3], those below N.
 __device__ inline void store4(const ProdArgs &a, int64_t i, int n, f32x4 v) {
   if (a.y_vec && n + 4 <= a.N) {
     if (a.y_bf16) {
       auto *to = (__attribute__((address_space(1))) uint64_t *)((uint16_t *)a.y + i * a.ldy + n);
       const uint64_t both = ((uint64_t)pack2_bf16(v[2], v[3]) << 32) | pack2_bf16(v[0], v[1]);
-      if constexpr (STREAM) __builtin_nontemporal_store(both, to);
-      else *to = both;
+      *to = both;
     } else {
       auto *to = (__attribute__((address_space(1))) f32x4_t *)((float *)a.y + i * a.ldy + n);
-      if constexpr (STREAM) __builtin_nontemporal_store((f32x4_t)v, to);
-      else *to = (f32x4_t)v;
+      *to = (f32x4_t)v;
     }
   } else {
 #pragma unroll
@@ -204,57 +202,124 @@ __device__ inline void store16(const ProdArgs &a, int64_t i, int n, const uint8_
   }
 }
 
+// ---- a row of an expert -------------------------------------------------------------------------
+// Bound by the weights, each read once for a row of x.  A wave takes R weight rows and meets them and
+// the row of x in runs of 1 KB, 16 bytes a lane: whole cache lines, several runs on their way at once.
+// The matrix instruction wants 16 rows of 64 bytes; it is given 16 pieces of 64 bytes of one row
+// instead, on both sides, and the 16 sums on the diagonal add up to the product (what lies beside it is
+// not used: the matrix cores have time to spare here).
+constexpr int kRun = 1024;
+
+template <Kind KIND, bool ON16>
+__device__ inline i32x4 run_at(const uint8_t *row, int k, int row_bytes) {
+  if constexpr (ON16) return k < row_bytes ? load16<true>((const int8_t *)row + k) : i32x4{0, 0, 0, 0};
+  else return chunk_at<KIND>(row, k, row_bytes);
+}
+
+template <Kind KIND, int R, bool ON16>
+__global__ __launch_bounds__(256) void k_product_vec(ProdArgs a, int cols) {
+  constexpr int kU = 12 / (R + 1) > 1 ? 12 / (R + 1) : 1;  // runs in flight
+  const Tiles tiles(a, 1, cols);
+  Where at;
+  if (!tiles.find(a, blockIdx.x % kXcds, blockIdx.x / kXcds, at)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (at.col * 4 + wave) * R, i0 = at.lo + at.tile;
+  const uint8_t *w[R], *we[R], *xe = nullptr;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int n = min(n0 + r, a.N - 1);
+    w[r] = a.w + at.expert * a.expert + n * a.ldw;
+    if constexpr (KIND == kMx) we[r] = a.we + at.expert * a.expert_e + n * a.ldwe;
+  }
+  const int src = source_of(a, i0);
+  const uint8_t *x = a.x + max(src, 0) * a.ldx;
+  if constexpr (KIND == kMx) xe = a.xe + max(src, 0) * a.ldxe;
+  f32x4 acc[R] = {};
+  for (int k0 = 0; k0 < a.row_bytes; k0 += kU * kRun) {
+    i32x4 W[kU][R], X[kU];
+    int sw[kU][R] = {}, sx[kU] = {};
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = k0 + u * kRun + lane * 16;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        W[u][r] = run_at<KIND, ON16>(w[r], k, a.row_bytes);
+        if constexpr (KIND == kMx) sw[u][r] = scale_at(we[r], k, a.row_bytes);
+      }
+      X[u] = run_at<KIND, ON16>(x, k, a.row_bytes);
+      if constexpr (KIND == kMx) sx[u] = scale_at(xe, k, a.row_bytes);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = mfma16<KIND>(W[u][r], X[u], sw[u][r], sx[u], acc[r]);
+  }
+  // the diagonal: lane l has rows 4 (l / 16) .. + 3 of column l % 16
+  const int d = lane & 15, e = d & 3;
+  const bool mine = d >> 2 == lane >> 4;
+  float out = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const f32x4 v = acc[r];
+    const float sum = wave_sum_to63(mine ? (e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3]) : 0.f);
+    const float all = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sum), 63));
+    out = lane == r ? all : out;
+  }
+  if (src < 0) out = __builtin_nanf("");
+  const int n = n0 + lane;
+  if (lane < R && n < a.N) {
+    if (a.y_bf16) store_el<true>(a.y, i0 * a.ldy + n, out);
+    else store_el<false>(a.y, i0 * a.ldy + n, out);
+  }
+}
+
 // ---- straight from memory -----------------------------------------------------------------
-// A workgroup takes 16 weight rows and 16 NT rows of one expert; its W waves share out the row's
-// steps of 64 bytes and add their sums in LDS in a fixed order.
-template <Kind KIND, int NT, int W>
-__global__ __launch_bounds__(64 * W) void k_product_few(ProdArgs a, int cols) {
-  __shared__ f32x4 s_acc[W][NT][64];
-  const Tiles tiles(a, 16 * NT, cols);
+// A workgroup takes 16 weight rows and 16 rows of one expert; its waves share out the row's steps of 64
+// bytes, four of them on their way at once, and add their sums in LDS in a fixed order.  Nothing is
+// staged, so a small product ends after little more than two trips to memory.
+template <Kind KIND, bool ON16>
+__global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
+  constexpr int kU = 4, kW = 8;
+  __shared__ f32x4 s_acc[kW][64];
+  const Tiles tiles(a, 16, cols);
   Where at;
   if (!tiles.find(a, blockIdx.x % kXcds, blockIdx.x / kXcds, at)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = at.col * 16, i0 = at.lo + at.tile * 16 * NT;
+  const int n0 = at.col * 16, i0 = at.lo + at.tile * 16;
   const int row = lane & 15, kq = (lane >> 4) * 16;
-  const int n = min(n0 + row, a.N - 1);
-  const uint8_t *w = a.w + at.expert * a.expert + n * a.ldw, *we = nullptr;
-  if constexpr (KIND == kMx) we = a.we + at.expert * a.expert_e + n * a.ldwe;
-  const uint8_t *x[NT], *xe[NT];
-  int src[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    src[t] = source_of(a, min(i0 + 16 * t + row, at.hi - 1));
-    x[t] = a.x + max(src[t], 0) * a.ldx;
-    if constexpr (KIND == kMx) xe[t] = a.xe + max(src[t], 0) * a.ldxe;
+  const int n = min(n0 + row, a.N - 1), src = source_of(a, min(i0 + row, at.hi - 1));
+  const uint8_t *w = a.w + at.expert * a.expert + n * a.ldw, *x = a.x + max(src, 0) * a.ldx, *we = nullptr, *xe = nullptr;
+  if constexpr (KIND == kMx) {
+    we = a.we + at.expert * a.expert_e + n * a.ldwe;
+    xe = a.xe + max(src, 0) * a.ldxe;
   }
-  f32x4 acc[NT] = {};
+  f32x4 acc = {};
   const int steps = (a.row_bytes + 63) / 64;
-  const int lo = (int)((int64_t)steps * wave / W), hi = (int)((int64_t)steps * (wave + 1) / W);
-#pragma unroll 2
-  for (int s = lo; s < hi; ++s) {
-    const int k = s * 64 + kq;
-    const i32x4 A = chunk_at<KIND>(w, k, a.row_bytes);
-    int sa = 0;
-    if constexpr (KIND == kMx) sa = scale_at(we, k, a.row_bytes);
+  const int lo = (int)((int64_t)steps * wave / kW), hi = (int)((int64_t)steps * (wave + 1) / kW);
+  for (int s = lo; s < hi; s += kU) {
+    i32x4 A[kU], B[kU];
+    int sa[kU] = {}, sb[kU] = {};
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const i32x4 B = chunk_at<KIND>(x[t], k, a.row_bytes);
-      int sb = 0;
-      if constexpr (KIND == kMx) sb = scale_at(xe[t], k, a.row_bytes);
-      acc[t] = mfma16<KIND>(A, B, sa, sb, acc[t]);
+    for (int u = 0; u < kU; ++u) {
+      const int k = s + u < hi ? (s + u) * 64 + kq : a.row_bytes;
+      A[u] = run_at<KIND, ON16>(w, k, a.row_bytes);
+      B[u] = run_at<KIND, ON16>(x, k, a.row_bytes);
+      if constexpr (KIND == kMx) {
+        sa[u] = scale_at(we, k, a.row_bytes);
+        sb[u] = scale_at(xe, k, a.row_bytes);
+      }
     }
-  }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) s_acc[wave][t][lane] = acc[t];
+    for (int u = 0; u < kU; ++u) acc = mfma16<KIND>(A[u], B[u], sa[u], sb[u], acc);
+  }
+  s_acc[wave][lane] = acc;
   __syncthreads();
-  for (int t = wave; t < NT; t += W) {
-    f32x4 sum = s_acc[0][t][lane];
+  if (wave) return;
 #pragma unroll
-    for (int v = 1; v < W; ++v) sum += s_acc[v][t][lane];
-    const int i = i0 + 16 * t + row, to = n0 + (lane >> 4) * 4;
-    if (src[t] < 0) sum = nan4();
-    if (i < at.hi && to < a.N) store4<false>(a, i, to, sum);
-  }
+  for (int v = 1; v < kW; ++v) acc += s_acc[v][lane];
+  const int i = i0 + row, to = n0 + (lane >> 4) * 4;
+  if (src < 0) acc = nan4();
+  if (i < at.hi && to < a.N) store4(a, i, to, acc);
 }
 
 // ---- through LDS ----------------------------------------------------------------------------
@@ -636,8 +701,17 @@ __global__ __launch_bounds__(kCopyThreads) void k_product_align(ProdArgs a, Copy
 }
 
 // ---- which kernel ---------------------------------------------------------------------------
-enum ProdKernel { kFew16, kFew32, kTile64, kTile128, kTile256 };
-constexpr int kRowsOf[] = {16, 32, 64, 128, 256};
+enum ProdKernel { kVec2, kVec8, kFew16, kTile32, kTile64, kTile128, kTile256, kKernels };
+struct Shape {
+  const char *name;
+  int rows, cols, threads;  // of a workgroup: rows of x, of weights
+  int together;             // tiles: workgroups on a compute unit
+};
+constexpr Shape kShapes[kKernels] = {{"product_vec2", 1, 8, 256, 0},      {"product_vec8", 1, 32, 256, 0},
+                                     {"product_few16", 16, 16, 512, 0},   {"product_tile32", 32, 64, 128, 2},
+                                     {"product_tile64", 64, 128, 256, 1}, {"product_tile128", 128, 128, 256, 2},
+                                     {"product_tile256", 256, 256, 256, 1}};
+constexpr int kUnits = 256;  // compute units
 
 struct ProdPlan {
   ProdKernel kernel;
@@ -649,19 +723,67 @@ bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && (E == 1 || expert % 16 == 0);
 }
 
+// The kernel with the least estimated time, fitted to 144 measured shapes (us, with the launch; of
+// them it takes the best kernel or one within 8% of it but for some twenty, and 3% more than the best on
+// average).  Every kernel waits for the weights of the experts that have rows, at about 5.4 TB/s.  The
+// direct kernels: a start, a trip to memory per step of K, and each further workgroup of a compute unit.
+// Tiles: for each round of them a start and end and a time per stage, which is shorter (`alone`) where
+// one has a compute unit to itself.  Grouped rows are thought to be spread evenly over the experts, which
+// they are not: a fifth more tiles.  Examples (vec2, vec8, few16, tile32, tile64, tile128, tile256):
+//   microscaled, 1 x 4096 x 2048                 3.5   4.5   4.3   5.4   6.4   8.7    12
+//   microscaled, 64 x 4096 x 6144                64    54    25    11    19    26     39
+//   microscaled, 1024 x 12288 x 2048             2570  1311  340   52    35    26     21
+//   bf16, 64 rows of 256 experts, 4096 x 2048    186   160   175   169   170   186    208
+//   bf16, 8192 of 256, 4096 x 2048               10466 6642  2512  847   783   807    865
+//   bf16, 32768 of 32, 2048 x 2048               15200 11625 3638  668   445   324    279
 ProdPlan plan_of(const ProdArgs &a, bool mx) {
+  struct Direct { double start, step, more, each; int bytes; };
+  static constexpr Direct kDirect[2][3] = {{{0, 0.43, 0.104, 0.29, 1024}, {0.53, 1.34, 0.46, 0, 1024}, {0, 0.031, 0.048, 0.39, 64}},
+                                           {{0.64, 0, 0.22, 0.47, 1024}, {1.2, 0.6, 0.95, 1.1, 1024}, {0.2, 0.085, 0.055, 0.3, 64}}};
+  struct Tile { double once, stage, alone; };
+  static constexpr Tile kTile[kKernels - kTile32] = {{1.15, 0.40, 0.26}, {1.73, 0.44, 0.40}, {1.92, 1.29, 0.76}, {6.1, 1.47, 1.15}};
   ProdPlan p{};
-  const int busy = a.first ? std::min(a.E, a.T) : 1;
-  const double rows = (double)a.T / busy;
-  // the tiles' offsets have 32 bits
-  const int64_t far = std::max({256 * a.ldw, 1024 * a.ldy, (a.order ? (int64_t)a.x_rows : 256) * a.ldx, 256 * a.ldwe, (a.order ? (int64_t)a.x_rows : 256) * a.ldxe});
-  p.kernel = rows < 16 ? kFew16 : rows < 40 ? kFew32 : rows < 100 ? kTile64 : rows < 400 ? kTile128 : kTile256;
-  if (far >> 32) p.kernel = kFew32;
-  if (p.kernel >= kTile64) {
-    const int64_t row = mx ? a.row_bytes / 16 : a.row_bytes;
-    const bool even = row % 16 == 0;
-    p.copy_x = !even || !(mx ? on16(a.xe, a.ldxe, a.x_rows, 0, 1) : on16(a.x, a.ldx, a.x_rows, 0, 1));
-    p.copy_w = !even || !(mx ? on16(a.we, a.ldwe, a.N, a.expert_e, a.E) : on16(a.w, a.ldw, a.N, a.expert, a.E));
+  const int64_t row = mx ? a.row_bytes / 16 : a.row_bytes;  // what may have to be copied
+  const bool even = row % 16 == 0;
+  const bool x_lies = even && (mx ? on16(a.xe, a.ldxe, a.x_rows, 0, 1) : on16(a.x, a.ldx, a.x_rows, 0, 1));
+  const bool w_lies = even && (mx ? on16(a.we, a.ldwe, a.N, a.expert_e, a.E) : on16(a.w, a.ldw, a.N, a.expert, a.E));
+  const double busy = a.first ? std::min<double>(a.T, a.E * (1 - std::exp(-(double)a.T / a.E))) : 1.0, each = a.T / busy;
+  const double weights = busy * a.N * a.row_bytes * (mx ? 17.0 / 16 : 1.0);
+  double best = 1e30;
+  for (int k = 0; k < kTile32; ++k) {
+    const Direct &d = kDirect[mx][k];
+    const Shape &s = kShapes[k];
+    const double steps = std::ceil((double)a.row_bytes / d.bytes), cols = std::ceil((double)a.N / s.cols);
+    const double tiles = s.rows == 1 ? a.T : a.first ? busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows);
+    const double n = tiles * cols / kUnits;
+    double us = 2.4 + std::max(d.start + d.step * steps + n * (d.more * steps + (a.first ? d.each : 0.0)), weights / (k == kVec2 ? 4.4e6 : 5.2e6));
+    if (!mx && !(x_lies && w_lies)) us *= 1.5;
+    if (us < best) {
+      best = us;
+      p.kernel = (ProdKernel)k;
+    }
+  }
+  // the tiles' offsets within an operand have 32 bits
+  const int64_t x_far = a.order ? (int64_t)a.x_rows : 256;
+  const bool near = !(std::max({256 * a.ldw, 256 * a.ldwe, x_far * a.ldx, x_far * a.ldxe, 1024 * a.ldy}) >> 32);
+  const double copied = (x_lies ? 0.0 : (double)a.x_rows * row) + (w_lies ? 0.0 : busy * a.N * row);
+  const double copy = (x_lies && w_lies) ? 0.0 : 3.0 * (!x_lies + !w_lies) + copied / 2e6;
+  for (int k = kTile32; near && k < kKernels; ++k) {
+    const Tile &t = kTile[k - kTile32];
+    const Shape &s = kShapes[k];
+    const double stages = std::ceil(a.row_bytes / 256.0) * 2, cols = std::ceil((double)a.N / s.cols);
+    const double tiles = cols * (a.first ? 1.2 * busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows));
+    const double n = std::ceil(tiles / kUnits);
+    const double us = copy + 2.5 + std::max(n == 1 ? t.once + t.alone * stages : std::ceil(n / s.together) * (t.once + t.stage * stages),
+                                            weights / 5.4e6 + 0.6 * t.once);
+    if (us < best) {
+      best = us;
+      p.kernel = (ProdKernel)k;
+    }
+  }
+  if (p.kernel >= kTile32) {
+    p.copy_x = !x_lies;
+    p.copy_w = !w_lies;
     p.ld = (row + 15) / 16 * 16;
     p.bytes_x = p.copy_x ? a.x_rows * p.ld : 0;
     p.bytes = p.bytes_x + (p.copy_w ? (int64_t)a.E * a.N * p.ld : 0);
@@ -678,27 +800,45 @@ unsigned blocks_of(const ProdArgs &a, int rows, int cols) {
   return (unsigned)((most_tiles(a, rows) * cols + kXcds - 1) / kXcds * kXcds);
 }
 
-template <Kind KIND, int NT>
+template <Kind KIND, int R, bool ON16>
+void launch_vec(const ProdArgs &a, hipStream_t st) {
+  const int cols = (a.N + 4 * R - 1) / (4 * R);
+  MOE_LAUNCH((k_product_vec<KIND, R, ON16>), dim3(blocks_of(a, 1, cols)), dim3(256), 0, st, a, cols);
+}
+template <Kind KIND, bool ON16>
 void launch_few(const ProdArgs &a, hipStream_t st) {
-  constexpr int W = 8;
   const int cols = (a.N + 15) / 16;
-  MOE_LAUNCH((k_product_few<KIND, NT, W>), dim3(blocks_of(a, 16 * NT, cols)), dim3(64 * W), 0, st, a, cols);
+  MOE_LAUNCH((k_product_few<KIND, ON16>), dim3(blocks_of(a, 16, cols)), dim3(512), 0, st, a, cols);
 }
 template <Kind KIND, int BN, int BS, int WN, int WS, int NBUF, int TOGETHER>
 void launch_tile(const ProdArgs &a, hipStream_t st) {
   const int cols = (a.N + BN - 1) / BN;
-  const unsigned most = 256 * TOGETHER;  // on the chip at once
+  const unsigned most = kUnits * TOGETHER;  // on the chip at once
   MOE_LAUNCH((k_product_tile<KIND, BN, BS, WN, WS, NBUF, TOGETHER>), dim3(std::min(blocks_of(a, BS, cols), most)), dim3(64 * WN * WS), 0, st, a, cols);
 }
 
+template <Kind KIND, bool ON16>
+void launch_direct(const ProdArgs &a, ProdKernel k, hipStream_t st) {
+  switch (k) {
+    case kVec2: launch_vec<KIND, 2, ON16>(a, st); break;
+    case kVec8: launch_vec<KIND, 8, ON16>(a, st); break;
+    default: launch_few<KIND, ON16>(a, st); break;
+  }
+}
 template <Kind KIND>
 void launch_piece(const ProdArgs &a, ProdKernel k, hipStream_t st) {
   switch (k) {
-    case kFew16: launch_few<KIND, 1>(a, st); break;
-    case kFew32: launch_few<KIND, 2>(a, st); break;
+    case kTile32: launch_tile<KIND, 64, 32, 2, 1, 4, 2>(a, st); break;
     case kTile64: launch_tile<KIND, 128, 64, 2, 2, 4, 1>(a, st); break;
     case kTile128: launch_tile<KIND, 128, 128, 2, 2, 2, 2>(a, st); break;
     case kTile256: launch_tile<KIND, 256, 256, 2, 2, 2, 1>(a, st); break;
+    default: {
+      // rows at multiples of 16 bytes (microscaled ones are), or of any bytes
+      const bool even = KIND == kMx || (a.row_bytes % 16 == 0 && on16(a.x, a.ldx, a.x_rows, 0, 1) && on16(a.w, a.ldw, a.N, a.expert, a.E));
+      if (even) launch_direct<KIND, true>(a, k, st);
+      else if constexpr (KIND == kBf16) launch_direct<KIND, false>(a, k, st);
+      break;
+    }
   }
 }
 
@@ -745,17 +885,18 @@ hipError_t launch_product(const ProdArgs &a0, bool mx, hipStream_t st) {
     (mx ? a.expert_e : a.expert) = (int64_t)a.N * p.ld;
   }
   if (!mx && (p.copy_x || p.copy_w)) a.row_bytes = (int)p.ld;
-  // A launch holds fewer than 2^32 threads: many weight rows go in pieces.  (Tiles of 16 rows, of 16
-  // weight rows and 512 threads each, are for up to 16 rows an expert, so that the quotient is at least 1.)
-  const int64_t step = std::max<int64_t>(1, ((int64_t)1 << 18) / most_tiles(a, kRowsOf[p.kernel])) * 256;
+  // Tiles are counted in 31 bits, and a launch of the direct kernels holds fewer than 2^32 threads: many
+  // weight rows go in pieces.
+  const Shape &s = kShapes[p.kernel];
+  const int64_t pieces = ((int64_t)1 << 30) / most_tiles(a, s.rows) / (s.together ? 1 : s.threads / 4);
+  const int64_t step = std::max<int64_t>(1, pieces) * s.cols;
   for (int64_t n = 0; n < a.N; n += step) {
     ProdArgs c = a;
     c.N = (int)std::min<int64_t>(step, a.N - n);
     c.w += n * a.ldw;
     if (mx) c.we += n * a.ldwe;
     c.y = (char *)a.y + n * ys;
-    static constexpr const char *kNames[] = {"product_few16", "product_few32", "product_tile64", "product_tile128", "product_tile256"};
-    ProfScope ps(kNames[p.kernel], st);
+    ProfScope ps(s.name, st);
     if (mx) launch_piece<kMx>(c, p.kernel, st);
     else launch_piece<kBf16>(c, p.kernel, st);
     const hipError_t err = hipGetLastError();
