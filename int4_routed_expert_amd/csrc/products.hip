@@ -378,11 +378,12 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
   // scales have not met again when the pair two further on is requested.
   constexpr int kScBufs = NBUF <= 3 ? 2 : 4;
   constexpr int kScAt = NBUF * kStage, kOutAt = kScAt + kScBufs * kScSize;
-  // A wave turns 32 rows of kLine bytes of outputs round at once: whole cache lines, or half ones where
-  // that lets two workgroups share a compute unit.
-  constexpr int kLine = TOGETHER == 1 || TOGETHER * (kOutAt + kWaves * 32 * 128) <= 160 * 1024 ? 128 : 64;
+  // A wave turns 32 rows of kLine bytes of outputs round at once: whole cache lines, or parts of them
+  // where LDS has no room for more.
+  constexpr int kRoom = 160 * 1024 / TOGETHER - kOutAt;
+  constexpr int kLine = kRoom >= kWaves * 32 * 128 ? 128 : kRoom >= kWaves * 32 * 64 ? 64 : 32;
   constexpr int kOut = 32 * kLine;
-  static_assert(TOGETHER * (kOutAt + kWaves * kOut) <= 160 * 1024, "LDS");
+  static_assert(kRoom >= kWaves * kOut, "LDS");
   __shared__ __align__(128) uint8_t s_buf[kOutAt + kWaves * kOut];
   const Tiles tiles(a, BS, cols);
   const int xcd = blockIdx.x % kXcds, apart = gridDim.x / kXcds;
@@ -594,7 +595,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
     auto leave = [&](auto bf16) __attribute__((always_inline)) {
       constexpr bool BF16 = decltype(bf16)::value;
       constexpr int kI = BF16 && TN > 1 && kLine == 128 ? 2 : 1;  // blocks of weights at once
-      constexpr int kE = !BF16 && kLine == 64 ? 2 : 4;             // quarters of a block at once
+      constexpr int kE = std::min(4, kLine / (BF16 ? 16 : 32));    // quarters of a block at once
       constexpr int kSize = BF16 ? 2 : 4, kEach = 16 / kSize;      // outputs of a 16-byte piece
       constexpr int kCh = kI * kE * 8 / kEach;                     // pieces of a row
       constexpr int kQ = kCh / 2;                                  // rows, and pieces, of a lane
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
                 f32x4 v = {acc[i + h][j][4 * e], acc[i + h][j][4 * e + 1], acc[i + h][j][4 * e + 2], acc[i + h][j][4 * e + 3]};
                 if (lost) v = f32x4{none, none, none, none};
                 if constexpr (BF16)
-                  *(uint64_t *)(piece(row, h * 4 + e) + ck * 8) = ((uint64_t)pack2_bf16(v[2], v[3]) << 32) | pack2_bf16(v[0], v[1]);
+                  *(uint64_t *)(piece(row, h * 4 + e - e0) + ck * 8) = ((uint64_t)pack2_bf16(v[2], v[3]) << 32) | pack2_bf16(v[0], v[1]);
                 else
                   *(f32x4 *)piece(row, 2 * (e - e0) + ck) = v;
               }
@@ -637,7 +638,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
                 const int r = r0 + lane / kCh + q * (64 / kCh);
                 auto *to = (__attribute__((address_space(1))) any *)(y + n * kSize + (uint32_t)(r * (int)b.ldy + lane % kCh * kEach) * kSize);
                 if (r < rows) {
-                  if (b.stream) put<16>((void *)to, v[q], true);
+                  if (kLine == 128 && b.stream) put<16>((void *)to, v[q], true);
                   else *to = v[q];
                 }
               }
@@ -701,7 +702,7 @@ __global__ __launch_bounds__(kCopyThreads) void k_product_align(ProdArgs a, Copy
 }
 
 // ---- which kernel ---------------------------------------------------------------------------
-enum ProdKernel { kVec2, kVec8, kFew16, kTile32, kTile64, kTile128, kTile256, kKernels };
+enum ProdKernel { kVec2, kVec8, kFew16, kTile32, kTile64, kTile128, kTile256x128, kTile256, kKernels };
 struct Shape {
   const char *name;
   int rows, cols, threads;  // of a workgroup: rows of x, of weights
@@ -710,7 +711,7 @@ struct Shape {
 constexpr Shape kShapes[kKernels] = {{"product_vec2", 1, 8, 256, 0},      {"product_vec8", 1, 32, 256, 0},
                                      {"product_few16", 16, 16, 512, 0},   {"product_tile32", 32, 64, 128, 2},
                                      {"product_tile64", 64, 128, 256, 1}, {"product_tile128", 128, 128, 256, 2},
-                                     {"product_tile256", 256, 256, 256, 1}};
+                                     {"product_tile256x128", 128, 256, 256, 1}, {"product_tile256", 256, 256, 256, 1}};
 constexpr int kUnits = 256;  // compute units
 
 struct ProdPlan {
@@ -723,25 +724,26 @@ bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && (E == 1 || expert % 16 == 0);
 }
 
-// The kernel with the least estimated time, fitted to 144 measured shapes (us, with the launch; of
-// them it takes the best kernel or one within 8% of it but for some twenty, and 3% more than the best on
-// average).  Every kernel waits for the weights of the experts that have rows, at about 5.4 TB/s.  The
-// direct kernels: a start, a trip to memory per step of K, and each further workgroup of a compute unit.
-// Tiles: for each round of them a start and end and a time per stage, which is shorter (`alone`) where
-// one has a compute unit to itself.  Grouped rows are thought to be spread evenly over the experts, which
-// they are not: a fifth more tiles.  Examples (vec2, vec8, few16, tile32, tile64, tile128, tile256):
-//   microscaled, 1 x 4096 x 2048                 3.5   4.5   4.3   5.4   6.4   8.7    12
-//   microscaled, 64 x 4096 x 6144                64    54    25    11    19    26     39
-//   microscaled, 1024 x 12288 x 2048             2570  1311  340   52    35    26     21
-//   bf16, 64 rows of 256 experts, 4096 x 2048    186   160   175   169   170   186    208
-//   bf16, 8192 of 256, 4096 x 2048               10466 6642  2512  847   783   807    865
-//   bf16, 32768 of 32, 2048 x 2048               15200 11625 3638  668   445   324    279
+// The kernel with the least estimated time, fitted to 152 measured shapes (us, with the launch; of
+// them it takes the best kernel or one within 8% of it but for sixteen, where it loses up to 46%, and
+// 2.3% on average).  Every kernel waits for the weights of the experts that have rows, at 5.2 to 5.6
+// TB/s.  The direct kernels: a start, a trip to memory per step of K, and each further workgroup of a
+// compute unit.  Tiles: for each round of them a start and end and a time per stage, `alone` where there
+// is one tile for a compute unit; this and the weights' time add up as squares.  Grouped rows are thought
+// to be spread evenly over the experts, which they are not: some more tiles.  Measured (vec2, vec8, few16,
+// tile32, tile64, tile128, tile256x128, tile256):
+//   microscaled, 1 x 4096 x 2048                 3.5   4.5   4.3  5.4  6.4  8.7  10   12
+//   microscaled, 64 x 4096 x 6144                64    54    25   11   19   26   32   39
+//   microscaled, 1024 x 12288 x 2048             2570  1311  340  52   35   26   22   21
+//   bf16, 64 rows of 256 experts, 4096 x 2048    186   160   175  169  170  186  201  208
+//   bf16, 16384 of 256, 4096 x 2048              20409 12817 4447 1148 919  872  775  943
+//   bf16, 32768 of 32, 2048 x 2048               15200 11625 3638 668  445  324  284  279
 ProdPlan plan_of(const ProdArgs &a, bool mx) {
   struct Direct { double start, step, more, each; int bytes; };
   static constexpr Direct kDirect[2][3] = {{{0, 0.43, 0.104, 0.29, 1024}, {0.53, 1.34, 0.46, 0, 1024}, {0, 0.031, 0.048, 0.39, 64}},
                                            {{0.64, 0, 0.22, 0.47, 1024}, {1.2, 0.6, 0.95, 1.1, 1024}, {0.2, 0.085, 0.055, 0.3, 64}}};
   struct Tile { double once, stage, alone; };
-  static constexpr Tile kTile[kKernels - kTile32] = {{1.15, 0.40, 0.26}, {1.73, 0.44, 0.40}, {1.92, 1.29, 0.76}, {6.1, 1.47, 1.15}};
+  static constexpr Tile kTile[kKernels - kTile32] = {{1.03, 0.33, 0.25}, {1.62, 0.33, 0.40}, {2.22, 0.93, 0.72}, {4.42, 0.68, 0.78}, {5.67, 1.05, 1.25}};
   ProdPlan p{};
   const int64_t row = mx ? a.row_bytes / 16 : a.row_bytes;  // what may have to be copied
   const bool even = row % 16 == 0;
@@ -772,15 +774,16 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
     const Tile &t = kTile[k - kTile32];
     const Shape &s = kShapes[k];
     const double stages = std::ceil(a.row_bytes / 256.0) * 2, cols = std::ceil((double)a.N / s.cols);
-    const double tiles = cols * (a.first ? 1.2 * busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows));
+    const double tiles = cols * (a.first ? 1.15 * busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows));
     const double n = std::ceil(tiles / kUnits);
-    const double us = copy + 2.5 + std::max(n == 1 ? t.once + t.alone * stages : std::ceil(n / s.together) * (t.once + t.stage * stages),
-                                            weights / 5.4e6 + 0.6 * t.once);
+    const double us = copy + 2.5 + std::hypot(n == 1 ? t.once + t.alone * stages : std::ceil(n / s.together) * (t.once + t.stage * stages),
+                                              weights / 5.6e6);
     if (us < best) {
       best = us;
       p.kernel = (ProdKernel)k;
     }
   }
+  if (!a.first && a.T == 1) p.kernel = kVec2;
   if (p.kernel >= kTile32) {
     p.copy_x = !x_lies;
     p.copy_w = !w_lies;
@@ -831,6 +834,7 @@ void launch_piece(const ProdArgs &a, ProdKernel k, hipStream_t st) {
     case kTile32: launch_tile<KIND, 64, 32, 2, 1, 4, 2>(a, st); break;
     case kTile64: launch_tile<KIND, 128, 64, 2, 2, 4, 1>(a, st); break;
     case kTile128: launch_tile<KIND, 128, 128, 2, 2, 2, 2>(a, st); break;
+    case kTile256x128: launch_tile<KIND, 256, 128, 2, 2, 3, 1>(a, st); break;
     case kTile256: launch_tile<KIND, 256, 256, 2, 2, 2, 1>(a, st); break;
     default: {
       // rows at multiples of 16 bytes (microscaled ones are), or of any bytes
