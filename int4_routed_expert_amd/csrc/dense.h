@@ -75,6 +75,12 @@ __device__ inline uint32_t pack2_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Of a wave-uniform address, through the scalar cache: for memory that the kernel does not write.
+template <class T>
+__device__ inline T ldk(const T *p) {
+  return *(const __attribute__((address_space(4))) T *)p;
+}
+
 template <bool BF16>
 __device__ inline float load_el(const void *p, int64_t i) {
   if constexpr (BF16) return bf16_f(ldg<uint16_t>((const uint16_t *)p + i));

@@ -14,7 +14,7 @@ namespace {
 // them; beyond, chunks are counted by one launch and placed by a second, each workgroup of
 // which adds up the counters of the chunks before its own.
 constexpr int kGroupWaves = 16, kGroupThreads = 64 * kGroupWaves;
-constexpr int kOnePairs = 8192;
+constexpr int kOnePairs = 2048;
 constexpr int kMostChunks = 256;
 
 __device__ inline int key_of(const GroupArgs &a, int p) {
@@ -184,20 +184,27 @@ __device__ inline void load_cols(const void *p, int64_t row, int c, int H, float
 
 template <bool BF16, bool ON16>
 __global__ __launch_bounds__(kCombineThreads) void k_combine(CombineArgs a, int parts) {
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 8;  // rows on their way at once
   const int64_t s = blockIdx.x / parts;
+  const int32_t *place = a.place + s * a.k;
+  const float *weight = a.w + s * a.k;
   const int c = (int)(blockIdx.x % parts) * kCombineCols + threadIdx.x * 8;
   if (c >= a.H) return;
-  float y[8] = {};
+  float y[8] = {}, last[8] = {};
+  if (a.add) load_cols<BF16, ON16>(a.add, s * a.lda, c, a.H, last);
   for (int j0 = 0; j0 < a.k; j0 += kAhead) {
     float v[kAhead][8] = {}, w[kAhead] = {};
+    int p[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (j0 + j >= a.k) break;
-      const int p = ldg<int32_t>(a.place + s * a.k + j0 + j);
-      if ((uint32_t)p >= (uint32_t)a.T) continue;
-      w[j] = ldg<float>(a.w + s * a.k + j0 + j);
-      load_cols<BF16, ON16>(a.z, p * a.ldz, c, a.H, v[j]);
+      const int at = min(j0 + j, a.k - 1);
+      p[j] = ldk(place + at);
+      w[j] = ldk(weight + at);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j < a.k && (uint32_t)p[j] < (uint32_t)a.T) load_cols<BF16, ON16>(a.z, p[j] * a.ldz, c, a.H, v[j]);
+      else w[j] = 0.f;
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
@@ -205,10 +212,8 @@ __global__ __launch_bounds__(kCombineThreads) void k_combine(CombineArgs a, int 
       for (int i = 0; i < 8; ++i) y[i] = fmaf(w[j], v[j][i], y[i]);
   }
   if (a.add) {
-    float v[8];
-    load_cols<BF16, ON16>(a.add, s * a.lda, c, a.H, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] += v[i];
+    for (int i = 0; i < 8; ++i) y[i] += last[i];
   }
   const int64_t to = s * a.ldy + c;
   if (ON16 && c + 8 <= a.H) {

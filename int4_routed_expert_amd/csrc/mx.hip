@@ -1,6 +1,7 @@
 // Microscaled rows (blocks of 32 e2m1 codes and one e8m0 scale) from rows or from a SwiGLU, and
 // back.
 #include <algorithm>
+#include <type_traits>
 
 #include "experts.h"
 
@@ -15,13 +16,18 @@ __device__ inline float silu_times(float g, float u) { return g / (1.0f + expf(-
 
 // Lane l of quad l / 4 takes eight neighbours, a quad a block: a wave reads and writes runs.
 // Units of eight are counted through all rows; a workgroup finds its first one's row, a lane
-// goes on from there in 32 bits.
+// goes on from there in 32 bits (without a division where a row has as many units as the
+// workgroup).
 struct Unit {
   int64_t row;
   int c;  // first element
 };
+template <int MOST>
 __device__ inline Unit unit_of(int64_t first_row, uint32_t first_unit, uint32_t i, uint32_t per_row) {
-  const uint32_t n = first_unit + i, r = n / per_row;
+  const uint32_t n = first_unit + i;
+  uint32_t r;
+  if (per_row >= MOST) r = n >= per_row;
+  else r = n / per_row;
   return {first_row + r, (int)(n - r * per_row) * 8};
 }
 
@@ -40,7 +46,16 @@ __device__ inline uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
 }
 
-// U units a thread.
+// A block's scale from m, the bits of its largest magnitude in fp32: m = 2^(field - 127) (1 +
+// fraction), so e = field - 2; over 1.5 times that it exceeds 6 2^(e-127).
+__device__ inline int scale_of(uint32_t m, int up) {
+  const int field = (int)(m >> 23);
+  return m >= kInfBits ? 255 : max(field - 2, 0) + (up && field >= 2 && (m & 0x7FFFFFu) > 0x400000u);
+}
+
+// U units a thread.  The conversion divides by its scale operand, a power of two, and rounds once, to
+// the even code at ties, magnitudes over 6 to 6.  With e = 0 that power is no normal number: values and
+// scale are raised by 2^126 first, which is exact.
 template <bool BF16, bool SILU, bool ON16, int U>
 __global__ __launch_bounds__(kMxThreads) void k_mx_quant(MxArgs a) {
   const uint32_t per_row = (uint32_t)(a.H + 31) / 32 * 4;
@@ -51,7 +66,7 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_quant(MxArgs a) {
   Unit at[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    at[i] = unit_of(r0, u0, i * kMxThreads + threadIdx.x, per_row);
+    at[i] = unit_of<kMxThreads * U>(r0, u0, i * kMxThreads + threadIdx.x, per_row);
     if (at[i].row < a.S) {
       load_unit<BF16, ON16>(a.x, at[i].row * a.ldx, at[i].c, a.H, v[i]);
       if constexpr (SILU) load_unit<BF16, ON16>(a.u, at[i].row * a.ldx, at[i].c, a.H, o[i]);
@@ -68,21 +83,19 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_quant(MxArgs a) {
     }
     m = quad_max<0xB1>(m);  // quad_perm [1,0,3,2]
     m = quad_max<0x4E>(m);  // quad_perm [2,3,0,1]
-    // m = 2^(field - 127) (1 + fraction), so e = field - 2; over 1.5 times that it exceeds 6 2^(e-127)
-    const int field = (int)(m >> 23);
-    int e = max(field - 2, 0) + (a.up && field >= 2 && (m & 0x7FFFFFu) > 0x400000u);
-    uint32_t w = 0;
-    if (m >= kInfBits) {
-      e = 255;
-    } else {
-      float s[8];
+    const int e = scale_of(m, a.up);
+    float s = __uint_as_float((uint32_t)e << 23);
+    if (__builtin_expect(e == 0, 0)) {
+      s = 0x1p-1f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = ldexpf(v[i][j], 127 - e);  // below 8: exact
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, s[0], s[1], 1.0f, 0);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, s[2], s[3], 1.0f, 1);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, s[4], s[5], 1.0f, 2);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, s[6], s[7], 1.0f, 3);
+      for (int j = 0; j < 8; ++j) v[i][j] *= 0x1p126f;
     }
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][0], v[i][1], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][2], v[i][3], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][4], v[i][5], s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[i][6], v[i][7], s, 3);
+    if (e == 255) w = 0;
     stg<uint32_t>(a.q + at[i].row * a.ldq + at[i].c / 2, w);
     if ((threadIdx.x & 3) == 0) stg<uint8_t>(a.e + at[i].row * a.lde + at[i].c / 32, (uint8_t)e);
   }
@@ -104,7 +117,7 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_values(MxArgs a) {
   Unit at[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    at[i] = unit_of(r0, u0, i * kMxThreads + threadIdx.x, per_row);
+    at[i] = unit_of<kMxThreads * U>(r0, u0, i * kMxThreads + threadIdx.x, per_row);
     if (at[i].row < a.S) {
       w[i] = ldg<uint32_t>(a.q + at[i].row * a.ldq + at[i].c / 2);
       e[i] = ldg<uint8_t>(a.e + at[i].row * a.lde + at[i].c / 32);
@@ -118,13 +131,15 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_values(MxArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = mx_value(w[i] >> (4 * j), scale);
     const int64_t to = at[i].row * a.ldy + at[i].c;
-    if (ON16 && at[i].c + 8 <= a.H) {
+    if (at[i].c + 8 <= a.H) {
       if constexpr (BF16) {
-        stg<uint4>((uint16_t *)a.y + to, make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]),
-                                                    pack2_bf16(v[6], v[7])));
+        typedef std::conditional_t<ON16, u32x4_t, u32x4_h> any;
+        const u32x4_t d = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
+        *(__attribute__((address_space(1))) any *)((uint16_t *)a.y + to) = d;
       } else {
-        stg<float4>((float *)a.y + to, make_float4(v[0], v[1], v[2], v[3]));
-        stg<float4>((float *)a.y + to + 4, make_float4(v[4], v[5], v[6], v[7]));
+        typedef std::conditional_t<ON16, f32x4_t, f32x4_w> any;
+        *(__attribute__((address_space(1))) any *)((float *)a.y + to) = f32x4_t{v[0], v[1], v[2], v[3]};
+        *(__attribute__((address_space(1))) any *)((float *)a.y + to + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
       }
     } else {
 #pragma unroll
@@ -143,14 +158,18 @@ int64_t rows_at_once(int64_t per_row) { return std::max<int64_t>(1, ((int64_t)1 
 // Few units: one a thread, so that they spread over the chip.
 constexpr int64_t kFewUnits = 256 * kMxThreads * 4;
 
+// Units a thread of many (8192 x 6144 bf16: 31.7 us with four, 34.0 with eight; SwiGLU 69.6 us with two,
+// 70.2 with four).
+template <bool SILU>
+constexpr int kMany = SILU ? 2 : 4;
 template <bool BF16, bool SILU, bool ON16>
 void launch_quant_one(const MxArgs &a, hipStream_t st) {
   const int64_t units = (int64_t)a.S * ((a.H + 31) / 32 * 4);
   if (units <= kFewUnits)
     MOE_LAUNCH((k_mx_quant<BF16, SILU, ON16, 1>), dim3((unsigned)((units + kMxThreads - 1) / kMxThreads)), dim3(kMxThreads), 0, st, a);
   else
-    MOE_LAUNCH((k_mx_quant<BF16, SILU, ON16, 4>), dim3((unsigned)((units + 4 * kMxThreads - 1) / (4 * kMxThreads))), dim3(kMxThreads), 0,
-               st, a);
+    MOE_LAUNCH((k_mx_quant<BF16, SILU, ON16, kMany<SILU>>), dim3((unsigned)((units + kMany<SILU> * kMxThreads - 1) / (kMany<SILU> * kMxThreads))),
+               dim3(kMxThreads), 0, st, a);
 }
 
 template <bool SILU>

@@ -81,11 +81,6 @@ struct Range {
   int lo, hi;
   __device__ int tiles(int rows) const { return hi > lo ? (hi - lo + rows - 1) / rows : 0; }
 };
-template <class T>
-__device__ inline T ldk(const T *p) {  // of a wave-uniform address, through the scalar cache: no kernel here writes there
-  return *(const __attribute__((address_space(4))) T *)p;
-}
-
 // Blocks go to the XCDs round-robin; each XCD gets a contiguous run of tiles, so that those in
 // flight on it share weights, and within an expert rows, in its L2.  An expert's tiles go in strips of
 // kStrip row tiles, column by column.
@@ -399,6 +394,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
   constexpr int kC = kBK / 16;
   static_assert(kThr / kC % 16 == 0, "chunks are mixed over 16 rows");
   const int kc = ((tid % kC) ^ mix_of(tid / kC)) << 4;
+  static_assert(BN % 64 == 0, "a wave's scales are of one operand");
   constexpr int kApart = kThr / kC;  // rows from one chunk of a thread to the next
   static_assert(BN % kApart == 0, "a load has rows of one operand");
   // A tile's operands by a base each (that of x its first row, or with order the whole of it) and a
@@ -425,8 +421,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
       xe_at = a.xe + x0 * a.ldxe;
 #pragma unroll
       for (int i = 0; i < kSc; ++i) {
-        // threads past the last row repeat their first load
-        const int r = tid + i * kThr < kRows ? tid + i * kThr : tid;
+        const int r = min(tid + i * kThr, kRows - 1);
         sc[i] = r < BN ? w_off(r) * (uint32_t)a.ldwe : x_off(r - BN) * (uint32_t)a.ldxe;
       }
     }
@@ -480,9 +475,9 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
       const bool in = s * 8 < sc_bytes;
 #pragma unroll
       for (int i = 0; i < kSc; ++i) {
-        const int r0 = wave * 64 + i * kThr < kRows ? i * kThr : 0;  // the wave's rows go from there
-        load_to_lds(__ballot(in), (wave * 64 + r0 < BN ? we_at : xe_at) + s * 8, sc[i], lds + sc_put + r0 * 16, kScAt);
-        if (!in) *(u32x4_t *)(s_buf + kScAt + sc_put + (tid + r0) * 16) = u32x4_t{0, 0, 0, 0};
+        const bool mine = tid + i * kThr < kRows;  // the others would write into the next buffer
+        load_to_lds(__ballot(in && mine), (wave * 64 + i * kThr < BN ? we_at : xe_at) + s * 8, sc[i], lds + sc_put, kScAt + i * kThr * 16);
+        if (!in && mine) *(u32x4_t *)(s_buf + kScAt + sc_put + (tid + i * kThr) * 16) = u32x4_t{0, 0, 0, 0};
       }
       sc_put = following(sc_put, kScSize, kScBufs);
     }

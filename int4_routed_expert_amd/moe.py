@@ -786,18 +786,20 @@ def _matrices(t, shape, what: str):
                      f"{tuple(t.shape)} with strides {tuple(t.stride())}")
 
 
-def _workspace_of(ws, need: int, like):
-    """(tensor, address, bytes) of the workspace given, or of a new one of `need` bytes."""
+def _workspace(ws):
+    """(address, bytes) of the workspace given, if any."""
     if ws is None:
-        if need <= 0:
-            return None, None, 0
-        ws = like.new_empty(need, dtype=torch.uint8)
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _contiguous_ws(ws) -> None:
-    if ws is not None and not ws.is_contiguous():
+        return None, 0
+    if not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous, not of strides {tuple(ws.stride())}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _missing(rc: int, ws, need: int, like):
+    """A new workspace, if that is what a call made without one was refused for (small calls need none, and are not asked)."""
+    if rc == MOE_ENULL and ws is None and need > 0:
+        return like.new_empty(need, dtype=torch.uint8)
+    return None
 
 
 def mx_quant(x, round_up: bool = False, stream=None):
@@ -883,7 +885,7 @@ def mx_matmul(q, e, w, ew, out_dtype=None, ws=None, stream=None):
     N, Bw, ldw, ldew = _codes(w, ew, "w")
     if Bw != B:
         raise ValueError(f"q has rows of {B} blocks, w of {Bw}")
-    _contiguous_ws(ws)
+    pws, nws = _workspace(ws)
     if (S | N | B) >> 31:
         _sizes("moe_mx_matmul", S, N, B)
     gpu = _gpu(q, e, w, ew, ws)
@@ -891,9 +893,12 @@ def mx_matmul(q, e, w, ew, out_dtype=None, ws=None, stream=None):
         return _elsewhere(gpu, stream, mx_matmul, (q, e, w, ew, ws), q, e, w, ew, out_dtype, ws)
     px = _MX_ROWS.pack(q.data_ptr(), e.data_ptr(), ldq, lde, 0, 0)
     pw = _MX_ROWS.pack(w.data_ptr(), ew.data_ptr(), ldw, ldew, 0, 0)
-    ws, pws, nws = _workspace_of(ws, _lib.moe_mx_matmul_workspace_bytes(px, pw, S, N, B), q)
     y = q.new_empty((S, N), dtype=out_dtype)
     rc = _lib.moe_mx_matmul(px, pw, S, N, B, y.data_ptr(), yd, N, pws, nws, _stream_of(gpu))
+    if rc == MOE_ENULL:
+        ws = _missing(rc, ws, _lib.moe_mx_matmul_workspace_bytes(px, pw, S, N, B), q)
+        if ws is not None:
+            rc = _lib.moe_mx_matmul(px, pw, S, N, B, y.data_ptr(), yd, N, ws.data_ptr(), ws.numel(), _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_mx_matmul")
     return y
@@ -905,16 +910,19 @@ def group(idx, n_experts: int, ws=None, stream=None):
     if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous():
         raise ValueError(f"idx must be a contiguous int32 matrix, not {tuple(idx.shape)} {idx.dtype}")
     S, k = idx.shape
-    _contiguous_ws(ws)
+    pws, nws = _workspace(ws)
     if (S | k | n_experts) >> 31:
         _sizes("moe_group", S, k, n_experts)
     gpu = _gpu(idx, ws)
     if stream is not None or gpu != _current_gpu():
         return _elsewhere(gpu, stream, group, (idx, ws), idx, n_experts, ws)
-    ws, pws, nws = _workspace_of(ws, _lib.moe_group_workspace_bytes(S, k, n_experts), idx)
     first, order, place = idx.new_empty(max(n_experts, 0) + 1), idx.new_empty(S * k), _empty_like(idx)
-    rc = _lib.moe_group(idx.data_ptr(), S, k, n_experts, first.data_ptr(), order.data_ptr(), place.data_ptr(), pws, nws,
-                        _stream_of(gpu))
+    args = idx.data_ptr(), S, k, n_experts, first.data_ptr(), order.data_ptr(), place.data_ptr()
+    rc = _lib.moe_group(*args, pws, nws, _stream_of(gpu))
+    if rc == MOE_ENULL:
+        ws = _missing(rc, ws, _lib.moe_group_workspace_bytes(S, k, n_experts), idx)
+        if ws is not None:
+            rc = _lib.moe_group(*args, ws.data_ptr(), ws.numel(), _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_group")
     return first, order, place
@@ -957,7 +965,7 @@ def grouped_matmul(x, w, first, order=None, top_k: int | None = None, out_dtype=
     E, N = w.shape[:2] if w.dim() == 3 else (0, 0)
     ldw, expert = _matrices(w, (E, N, K), "w")
     T, plan = _groups(first, order, top_k, E, rows)
-    _contiguous_ws(ws)
+    pws, nws = _workspace(ws)
     if (rows | T | N | K) >> 31:
         _sizes("moe_grouped_matmul", rows, T, N, K)
     if out_dtype is not None:
@@ -969,9 +977,12 @@ def grouped_matmul(x, w, first, order=None, top_k: int | None = None, out_dtype=
     over = out
     out, ldy, yd = _grouped_out(out, T, N, out_dtype, x)
     px, pw = x.data_ptr(), w.data_ptr()
-    ws, pws, nws = _workspace_of(ws, _lib.moe_grouped_matmul_workspace_bytes(px, ldx, rows, pw, ldw, expert, plan, T, N, K), x)
-    rc = _lib.moe_grouped_matmul(px, ldx, rows, pw, ldw, expert, plan, T, N, K, out.data_ptr(), yd, ldy, pws, nws,
-                                 _stream_of(gpu))
+    args = px, ldx, rows, pw, ldw, expert, plan, T, N, K
+    rc = _lib.moe_grouped_matmul(*args, out.data_ptr(), yd, ldy, pws, nws, _stream_of(gpu))
+    if rc == MOE_ENULL:
+        ws = _missing(rc, ws, _lib.moe_grouped_matmul_workspace_bytes(*args), x)
+        if ws is not None:
+            rc = _lib.moe_grouped_matmul(*args, out.data_ptr(), yd, ldy, ws.data_ptr(), ws.numel(), _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_grouped_matmul")
     if over is not None:
@@ -990,7 +1001,7 @@ def mx_grouped_matmul(q, e, w, ew, first, order=None, top_k: int | None = None, 
     ldw, expert = _matrices(w, (E, N, 16 * B), "w")
     ldew, expert_e = _matrices(ew, (E, N, B), "w's scales")
     T, plan = _groups(first, order, top_k, E, rows)
-    _contiguous_ws(ws)
+    pws, nws = _workspace(ws)
     if (rows | T | N | B) >> 31:
         _sizes("moe_mx_grouped_matmul", rows, T, N, B)
     if out_dtype is not None:
@@ -1003,8 +1014,12 @@ def mx_grouped_matmul(q, e, w, ew, first, order=None, top_k: int | None = None, 
     out, ldy, yd = _grouped_out(out, T, N, out_dtype, q)
     px = _MX_ROWS.pack(q.data_ptr(), e.data_ptr(), ldq, lde, 0, 0)
     pw = _MX_ROWS.pack(w.data_ptr(), ew.data_ptr(), ldw, ldew, expert, expert_e)
-    ws, pws, nws = _workspace_of(ws, _lib.moe_mx_grouped_matmul_workspace_bytes(px, rows, pw, plan, T, N, B), q)
-    rc = _lib.moe_mx_grouped_matmul(px, rows, pw, plan, T, N, B, out.data_ptr(), yd, ldy, pws, nws, _stream_of(gpu))
+    args = px, rows, pw, plan, T, N, B
+    rc = _lib.moe_mx_grouped_matmul(*args, out.data_ptr(), yd, ldy, pws, nws, _stream_of(gpu))
+    if rc == MOE_ENULL:
+        ws = _missing(rc, ws, _lib.moe_mx_grouped_matmul_workspace_bytes(*args), q)
+        if ws is not None:
+            rc = _lib.moe_mx_grouped_matmul(*args, out.data_ptr(), yd, ldy, ws.data_ptr(), ws.numel(), _stream_of(gpu))
     if rc:
         raise MoeError(rc, "moe_mx_grouped_matmul")
     if over is not None:
