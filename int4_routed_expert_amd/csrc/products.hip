@@ -426,7 +426,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
       }
     }
     lost = 0;
-    if (a.order) {
+    if (a.order || a.x_rows < a.T) {
 #pragma unroll
       for (int j = 0; j < TS; ++j) lost |= (x_row((wsv + WS * j) * 32 + row) < 0 ? 1u : 0u) << j;
     }
@@ -761,8 +761,9 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
     }
   }
   // the tiles' offsets within an operand have 32 bits
-  const int64_t x_far = a.order ? (int64_t)a.x_rows : 256;
-  const bool near = !(std::max({256 * a.ldw, 256 * a.ldwe, x_far * a.ldx, x_far * a.ldxe, 1024 * a.ldy}) >> 32);
+  p.ld = (row + 15) / 16 * 16;
+  const int64_t x_far = a.order ? (int64_t)a.x_rows : 256, ldx = x_lies ? 0 : p.ld, ldw = w_lies ? 0 : p.ld;
+  const bool near = !(std::max({256 * std::max({a.ldw, a.ldwe, ldw}), x_far * std::max({a.ldx, a.ldxe, ldx}), 1024 * a.ldy}) >> 32);
   const double copied = (x_lies ? 0.0 : (double)a.x_rows * row) + (w_lies ? 0.0 : busy * a.N * row);
   const double copy = (x_lies && w_lies) ? 0.0 : 3.0 * (!x_lies + !w_lies) + copied / 2e6;
   for (int k = kTile32; near && k < kKernels; ++k) {
@@ -782,7 +783,6 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
   if (p.kernel >= kTile32) {
     p.copy_x = !x_lies;
     p.copy_w = !w_lies;
-    p.ld = (row + 15) / 16 * 16;
     p.bytes_x = p.copy_x ? a.x_rows * p.ld : 0;
     p.bytes = p.bytes_x + (p.copy_w ? (int64_t)a.E * a.N * p.ld : 0);
   }

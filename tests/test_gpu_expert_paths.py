@@ -179,6 +179,32 @@ def test_poison_stays_in_its_rows(M, T, E, N, K):
     assert torch.equal(torch.nan_to_num(got, nan=1e30), torch.nan_to_num(want, nan=1e30))
 
 
+@pytest.mark.parametrize("T,E,N,K", [(8, 40, 4000, 4096), (20, 10, 500, 512), (60, 40, 600, 512), (600, 12, 4000, 4096),
+                                     (1500, 12, 4000, 512)])
+@pytest.mark.parametrize("short", [1, 7])
+def test_rows_beyond_x_are_nan(M, T, E, N, K, short):
+    """A call without order whose x has fewer rows than y."""
+    g = rng(T)
+    first = first_of(counts(T, E))
+    rows = T - short
+    x = torch.full((T, K), 3.0, device="cuda").to(BF)
+    x[:rows] = torch.randint(-4, 5, (rows, K), generator=g, device="cuda").to(BF)
+    w = torch.randint(-4, 5, (E, N, K), generator=g, device="cuda").to(BF)
+    want = R.product(x.double(), w.double(), first.tolist(), torch.zeros(T, N, dtype=torch.float64, device="cuda"))
+    plan = M.moe_groups(first.data_ptr(), None, E, 0)
+    y = torch.zeros(T, N, device="cuda")
+    M.moe_grouped_matmul(x, K, rows, w, K, N * K, plan, T, N, K, y, M.MOE_F32, N, None, 0)
+    assert torch.equal(y[:rows].double(), want[:rows]) and torch.isnan(y[rows:]).all()
+    q, e = M.mx_quant(x)
+    v, ve = M.mx_quant(w.view(E * N, K))
+    want = R.product(R.values(q, e), R.values(v, ve).view(E, N, K), first.tolist(), want)
+    y = torch.zeros(T, N, device="cuda")
+    a = M.moe_mx_rows(q.data_ptr(), e.data_ptr(), K // 2, K // 32, 0, 0)
+    b = M.moe_mx_rows(v.data_ptr(), ve.data_ptr(), K // 2, K // 32, N * K // 2, N * K // 32)
+    M.moe_mx_grouped_matmul(a, rows, b, plan, T, N, K // 32, y, M.MOE_F32, N, None, 0)
+    assert torch.equal(y[:rows].double(), want[:rows]) and torch.isnan(y[rows:]).all()
+
+
 @pytest.mark.parametrize("E", [1, 63, 65, 1000, 1024])
 def test_many_experts(M, E):
     """One lane of the search has up to sixteen experts; most have no rows."""
