@@ -172,15 +172,38 @@ int64_t chunks_of(int64_t T) { return T <= kOnePairs ? 1 : std::min<int64_t>(kMo
 // bytes and adds them up in the order of j.
 constexpr int kCombineThreads = 256, kCombineCols = 8 * kCombineThreads;
 
-template <bool BF16, bool ON16>
-__device__ inline void load_cols(const void *p, int64_t row, int c, int H, float *v) {
-  if (c + 8 <= H) {
-    load8<BF16, ON16>(p, row + c, v);
-  } else {
+// Eight columns of a row as they lie (bf16 two to a word), those below H; they are made numbers when they
+// are added up, so that few registers hold many rows on their way.
+template <bool BF16>
+struct Cols {
+  static constexpr int kWords = BF16 ? 4 : 8;
+  uint32_t d[kWords];
+
+  template <bool ON16>
+  __device__ inline void load(const void *p, int64_t row, int c, int H) {
+    if (c + 8 <= H) {
+      if constexpr (BF16 && ON16) {
+        const uint4 r = ldg<uint4>((const uint16_t *)p + row + c);
+        d[0] = r.x; d[1] = r.y; d[2] = r.z; d[3] = r.w;
+      } else {
+        float v[8];
+        load8<BF16, ON16>(p, row + c, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < H ? load_el<BF16>(p, row + c + j) : 0.f;
+        for (int i = 0; i < kWords; ++i) d[i] = BF16 ? __float_as_uint(v[2 * i]) >> 16 | __float_as_uint(v[2 * i + 1]) : __float_as_uint(v[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) d[i] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < H) d[BF16 ? i / 2 : i] |= __float_as_uint(load_el<BF16>(p, row + c + i)) >> (BF16 && i % 2 == 0 ? 16 : 0);
+    }
   }
-}
+  __device__ inline float at(int i) const {
+    if constexpr (BF16) return __uint_as_float(i % 2 ? d[i / 2] & 0xFFFF0000u : d[i / 2] << 16);
+    else return __uint_as_float(d[i]);
+  }
+};
 
 template <bool BF16, bool ON16>
 __global__ __launch_bounds__(kCombineThreads) void k_combine(CombineArgs a, int parts) {
@@ -190,10 +213,11 @@ __global__ __launch_bounds__(kCombineThreads) void k_combine(CombineArgs a, int 
   const float *weight = a.w + s * a.k;
   const int c = (int)(blockIdx.x % parts) * kCombineCols + threadIdx.x * 8;
   if (c >= a.H) return;
-  float y[8] = {}, last[8] = {};
-  if (a.add) load_cols<BF16, ON16>(a.add, s * a.lda, c, a.H, last);
+  float y[8] = {};
+  Cols<BF16> last;
   for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-    float v[kAhead][8] = {}, w[kAhead] = {};
+    Cols<BF16> v[kAhead];
+    float w[kAhead];
     int p[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -202,18 +226,19 @@ __global__ __launch_bounds__(kCombineThreads) void k_combine(CombineArgs a, int 
       w[j] = ldk(weight + at);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (j0 + j < a.k && (uint32_t)p[j] < (uint32_t)a.T) load_cols<BF16, ON16>(a.z, p[j] * a.ldz, c, a.H, v[j]);
-      else w[j] = 0.f;
-    }
+    for (int j = 0; j < kAhead; ++j)
+      if (j0 + j < a.k && (uint32_t)p[j] < (uint32_t)a.T) v[j].template load<ON16>(a.z, p[j] * a.ldz, c, a.H);
+    if (a.add && j0 + kAhead >= a.k) last.template load<ON16>(a.add, s * a.lda, c, a.H);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
+      if (j0 + j < a.k && (uint32_t)p[j] < (uint32_t)a.T) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(w[j], v[j][i], y[i]);
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(w[j], v[j].at(i), y[i]);
+      }
   }
   if (a.add) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] += last[i];
+    for (int i = 0; i < 8; ++i) y[i] += last.at(i);
   }
   const int64_t to = s * a.ldy + c;
   if (ON16 && c + 8 <= a.H) {

@@ -672,28 +672,37 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
 }
 
 // ---- rows on 16-byte boundaries -------------------------------------------------------------
-// Copies rows to the workspace, each at a multiple of 16 bytes and filled up with zeros to one: the
-// loads into LDS need that.  A lane moves 16 bytes.  Rows of experts that have none to compute are
-// left out.
+// Copies the rows of x, of the weights or of both to the workspace, each at a multiple of 16 bytes and
+// filled up with zeros to one: the loads into LDS need that.  A lane moves 16 bytes.  Rows of experts that
+// have none to compute are left out.
 struct Copy {
   const uint8_t *from;
   uint8_t *to;
   int64_t ld, expert;  // bytes between the source's rows and experts
-  int64_t begin, end;  // 16-byte pieces of this launch
-  int N, row_bytes, chunks;
+  int64_t pieces;      // of 16 bytes
+  int N;               // rows of an expert
+};
+struct Copies {
+  Copy x, w;
+  int64_t begin;  // the pieces of this launch, x's first
+  int row_bytes, chunks;
 };
 constexpr int kCopyThreads = 256;
-__global__ __launch_bounds__(kCopyThreads) void k_product_align(ProdArgs a, Copy c) {
-  const int64_t block0 = c.begin + (int64_t)blockIdx.x * kCopyThreads;
+__global__ __launch_bounds__(kCopyThreads) void k_product_align(ProdArgs a, Copies c) {
+  int64_t block0 = c.begin + (int64_t)blockIdx.x * kCopyThreads;
+  const int64_t x_blocks = (c.x.pieces + kCopyThreads - 1) / kCopyThreads * kCopyThreads;
+  const bool w = block0 >= x_blocks;
+  const Copy &p = w ? c.w : c.x;
+  if (w) block0 -= x_blocks;
+  if (block0 + threadIdx.x >= p.pieces) return;
   const int64_t r0 = block0 / c.chunks;
   const uint32_t u = (uint32_t)(block0 - r0 * c.chunks) + threadIdx.x;
-  if (block0 + threadIdx.x >= c.end) return;
   const int64_t r = r0 + u / c.chunks;
   const int k = (int)(u % c.chunks) * 16;
-  const int64_t e = r / c.N;
-  if (a.first && c.expert && ldg<int32_t>(a.first + e) >= ldg<int32_t>(a.first + e + 1)) return;
-  const i32x4 v = load16_tail((const int8_t *)c.from + e * c.expert + (r - e * c.N) * c.ld, k, c.row_bytes);
-  stg<uint4>(c.to + (block0 + threadIdx.x) * 16, make_uint4((uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]));
+  const int64_t e = r / p.N;
+  if (w && a.first && ldg<int32_t>(a.first + e) >= ldg<int32_t>(a.first + e + 1)) return;
+  const i32x4 v = load16_tail((const int8_t *)p.from + e * p.expert + (r - e * p.N) * p.ld, k, c.row_bytes);
+  stg<uint4>(p.to + (block0 + threadIdx.x) * 16, make_uint4((uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]));
 }
 
 // ---- which kernel ---------------------------------------------------------------------------
@@ -720,8 +729,8 @@ bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
 }
 
 // The kernel with the least estimated time, fitted to 152 measured shapes (us, with the launch; of
-// them it takes the best kernel or one within 8% of it but for sixteen, where it loses up to 46%, and
-// 2.3% on average).  Every kernel waits for the weights of the experts that have rows, at 5.2 to 5.6
+// them it takes the best kernel or one within 8% of it but for eleven, where it loses up to 25%, and
+// 1.4% on average).  Every kernel waits for the weights of the experts that have rows, at 4.4 to 5.6
 // TB/s.  The direct kernels: a start, a trip to memory per step of K, and each further workgroup of a
 // compute unit.  Tiles: for each round of them a start and end and a time per stage, `alone` where there
 // is one tile for a compute unit; this and the weights' time add up as squares.  Grouped rows are thought
@@ -734,9 +743,10 @@ bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
 //   bf16, 16384 of 256, 4096 x 2048              20409 12817 4447 1148 919  872  775  943
 //   bf16, 32768 of 32, 2048 x 2048               15200 11625 3638 668  445  324  284  279
 ProdPlan plan_of(const ProdArgs &a, bool mx) {
-  struct Direct { double start, step, more, each; int bytes; };
-  static constexpr Direct kDirect[2][3] = {{{0, 0.43, 0.104, 0.29, 1024}, {0.53, 1.34, 0.46, 0, 1024}, {0, 0.031, 0.048, 0.39, 64}},
-                                           {{0.64, 0, 0.22, 0.47, 1024}, {1.2, 0.6, 0.95, 1.1, 1024}, {0.2, 0.085, 0.055, 0.3, 64}}};
+  struct Direct { double start, step, more, each, grouped, rate; int bytes; };
+  static constexpr Direct kDirect[2][3] = {
+      {{0, 0.734, 0.094, 0.262, 0, 4.4e6, 1024}, {0.264, 1.811, 0.441, 0, 0, 4.9e6, 1024}, {0.835, 0.052, 0.048, 0.438, 0, 5.2e6, 64}},
+      {{0.491, 0.082, 0.09, 0.25, 0.4, 4.4e6, 1024}, {1.1, 1.05, 0.9, 0.6, 0.6, 5.2e6, 1024}, {0.471, 0.101, 0.095, 0.274, 0.093, 5.2e6, 64}}};
   struct Tile { double once, stage, alone; };
   static constexpr Tile kTile[kKernels - kTile32] = {{1.03, 0.33, 0.25}, {1.62, 0.33, 0.40}, {2.22, 0.93, 0.72}, {4.42, 0.68, 0.78}, {5.67, 1.05, 1.25}};
   ProdPlan p{};
@@ -752,8 +762,8 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
     const Shape &s = kShapes[k];
     const double steps = std::ceil((double)a.row_bytes / d.bytes), cols = std::ceil((double)a.N / s.cols);
     const double tiles = s.rows == 1 ? a.T : a.first ? busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows);
-    const double n = tiles * cols / kUnits;
-    double us = 2.4 + std::max(d.start + d.step * steps + n * (d.more * steps + (a.first ? d.each : 0.0)), weights / (k == kVec2 ? 4.4e6 : 5.2e6));
+    const double n = std::ceil(tiles * cols / kUnits) - 1;
+    double us = 2.4 + std::max(d.start + d.step * steps + n * (d.more * steps + d.each + (a.first ? d.grouped : 0.0)), weights / d.rate);
     if (!mx && !(x_lies && w_lies)) us *= 1.5;
     if (us < best) {
       best = us;
@@ -765,7 +775,7 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
   const int64_t x_far = a.order ? (int64_t)a.x_rows : 256, ldx = x_lies ? 0 : p.ld, ldw = w_lies ? 0 : p.ld;
   const bool near = !(std::max({256 * std::max({a.ldw, a.ldwe, ldw}), x_far * std::max({a.ldx, a.ldxe, ldx}), 1024 * a.ldy}) >> 32);
   const double copied = (x_lies ? 0.0 : (double)a.x_rows * row) + (w_lies ? 0.0 : busy * a.N * row);
-  const double copy = (x_lies && w_lies) ? 0.0 : 3.0 * (!x_lies + !w_lies) + copied / 2e6;
+  const double copy = x_lies && w_lies ? 0.0 : 3.0 + copied / 2e6;
   for (int k = kTile32; near && k < kKernels; ++k) {
     const Tile &t = kTile[k - kTile32];
     const Shape &s = kShapes[k];
@@ -841,18 +851,28 @@ void launch_piece(const ProdArgs &a, ProdKernel k, hipStream_t st) {
   }
 }
 
-hipError_t launch_copy(const ProdArgs &a, const uint8_t *from, uint8_t *to, int64_t ld, int64_t expert, int64_t rows, int N,
-                       int row_bytes, hipStream_t st) {
-  Copy c{from, to, ld, expert, 0, 0, N, row_bytes, (row_bytes + 15) / 16};
-  const int64_t units = rows * c.chunks;
-  constexpr int64_t kMost = (int64_t)1 << 30;  // a launch holds fewer than 2^32 threads
-  for (c.begin = 0; c.begin < units; c.begin += kMost) {
-    c.end = std::min(units, c.begin + kMost);
+// Copies what the plan says, and points the arguments at it.
+hipError_t launch_copies(ProdArgs &a, const ProdPlan &p, bool mx, hipStream_t st) {
+  Copies c{};
+  c.row_bytes = mx ? a.row_bytes / 16 : a.row_bytes;
+  c.chunks = (int)(p.ld / 16);
+  const uint8_t *&x = mx ? a.xe : a.x, *&w = mx ? a.we : a.w;
+  int64_t &ldx = mx ? a.ldxe : a.ldx, &ldw = mx ? a.ldwe : a.ldw, &expert = mx ? a.expert_e : a.expert;
+  c.x = {x, a.ws, ldx, 0, p.copy_x ? (int64_t)a.x_rows * c.chunks : 0, a.x_rows};
+  c.w = {w, a.ws + p.bytes_x, ldw, expert, p.copy_w ? (int64_t)a.E * a.N * c.chunks : 0, a.N};
+  auto blocks = [](int64_t pieces) { return (pieces + kCopyThreads - 1) / kCopyThreads; };
+  const int64_t all = blocks(c.x.pieces) + blocks(c.w.pieces);
+  constexpr int64_t kMost = 1 << 22;  // a launch holds fewer than 2^32 threads
+  for (int64_t b = 0; b < all; b += kMost) {
+    c.begin = b * kCopyThreads;
     ProfScope ps("product_align", st);
-    MOE_LAUNCH(k_product_align, dim3((unsigned)((c.end - c.begin + kCopyThreads - 1) / kCopyThreads)), dim3(kCopyThreads), 0, st, a, c);
+    MOE_LAUNCH(k_product_align, dim3((unsigned)std::min(kMost, all - b)), dim3(kCopyThreads), 0, st, a, c);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
+  if (p.copy_x) x = a.ws, ldx = p.ld;
+  if (p.copy_w) w = a.ws + p.bytes_x, ldw = p.ld, expert = (int64_t)a.N * p.ld;
+  if (!mx) a.row_bytes = (int)p.ld;
   return hipSuccess;
 }
 
@@ -867,23 +887,10 @@ hipError_t launch_product(const ProdArgs &a0, bool mx, hipStream_t st) {
   // past the caches only whole 16-byte pieces
   a.stream = (int64_t)a.T * a.N * ys > kStreamBytes && (uintptr_t)a.y % 16 == 0 && a.ldy * ys % 16 == 0;
   const ProdPlan p = plan_of(a, mx);
-  const int row = mx ? a.row_bytes / 16 : a.row_bytes;
-  if (p.copy_x) {
-    const hipError_t err = launch_copy(a, mx ? a.xe : a.x, a.ws, mx ? a.ldxe : a.ldx, 0, a.x_rows, a.x_rows, row, st);
+  if (p.copy_x || p.copy_w) {
+    const hipError_t err = launch_copies(a, p, mx, st);
     if (err != hipSuccess) return err;
-    (mx ? a.xe : a.x) = a.ws;
-    (mx ? a.ldxe : a.ldx) = p.ld;
   }
-  if (p.copy_w) {
-    uint8_t *to = a.ws + p.bytes_x;
-    const hipError_t err = launch_copy(a, mx ? a.we : a.w, to, mx ? a.ldwe : a.ldw, mx ? a.expert_e : a.expert,
-                                       (int64_t)a.E * a.N, a.N, row, st);
-    if (err != hipSuccess) return err;
-    (mx ? a.we : a.w) = to;
-    (mx ? a.ldwe : a.ldw) = p.ld;
-    (mx ? a.expert_e : a.expert) = (int64_t)a.N * p.ld;
-  }
-  if (!mx && (p.copy_x || p.copy_w)) a.row_bytes = (int)p.ld;
   // Tiles are counted in 31 bits, and a launch of the direct kernels holds fewer than 2^32 threads: many
   // weight rows go in pieces.
   const Shape &s = kShapes[p.kernel];

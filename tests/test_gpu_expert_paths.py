@@ -52,9 +52,9 @@ def first_of(c):
 
 
 GROUPED = [  # kernel (of the microscaled product / of the bf16 one), T, E, N, K of each (None: not among these)
-    ("vec2", 1, 4, 100, 1024, 512), ("vec8", 8, 40, 4000, 4096, 2048), ("few16", 20, 10, 500, 512, 512),
+    ("vec2", 1, 4, 100, 1024, 512), ("vec8", 8, 40, 4000, 4096, 2048), ("few16/vec2", 20, 10, 500, 512, 512),
     ("few16", 20, 40, 1000, 256, None), ("tile32", 60, 40, 1500, 1536, None), ("tile32", 300, 10, 1000, 6144, 512),
-    ("few16/tile64", 300, 12, 2000, 544, 264), ("tile64", 500, 10, 2000, 1024, 1024), ("tile64", 330, 12, 2050, 2080, 1000),
+    ("tile64", 300, 12, 2000, 544, 264), ("tile64", 500, 10, 2000, 1024, 1024), ("tile64", 330, 12, 2050, 2080, 1000),
     ("tile64", 900, 20, 4000, 2080, 2081), ("tile128", 2000, 20, 2000, 512, 512), ("tile128", 2000, 20, 2001, 96, 40),
     ("tile128/tile256x128", 600, 12, 4000, 1056, 1050), ("tile256x128", 600, 12, 4000, 4096, 1024),
     ("tile256x128", 601, 12, 4011, 4192, 1032), ("tile256x128", 1500, 12, 6000, 2080, 1050), ("tile128/tile256", 1500, 12, 4000, 256, 512),
@@ -89,8 +89,8 @@ def test_grouped_kernels(M, kernel, T, E, N, K, gather, mx):
         assert f"product_{kernel}" in names, names
 
 
-MX = [("vec2", 1, 333, 70), ("few16", 5, 500, 20), ("tile32", 90, 5000, 32), ("tile32", 300, 2000, 64), ("few16", 600, 3000, 17),
-      ("few16", 100, 12000, 8), ("tile64", 600, 3000, 16), ("tile128", 2000, 6000, 16), ("tile128", 200, 16000, 33),
+MX = [("vec2", 1, 333, 70), ("vec2", 5, 500, 20), ("few16", 70, 600, 20), ("tile32", 90, 5000, 32), ("tile32", 300, 2000, 64), ("tile64", 600, 3000, 17),
+      ("tile64", 100, 12000, 8), ("tile64", 600, 3000, 16), ("tile128", 2000, 6000, 16), ("tile128", 200, 16000, 33),
       ("tile128", 300, 9000, 67), ("tile128", 2500, 4001, 9), ("tile256x128", 600, 7000, 128), ("tile256x128", 600, 7000, 131),
       ("tile256", 1500, 20000, 16), ("tile256", 1000, 12001, 17), ("tile256", 700, 12000, 67)]
 
