@@ -49,9 +49,9 @@ typedef struct moe_groups {
  * sizes), for the rows i < T of y that belong to an expert.  Other rows of y, those from
  * first[n] on, are left as they were.  x: [x_rows, K] bf16, rows ldx elements apart; w: [n, N, K]
  * bf16, rows ldw and experts `expert` elements apart; y: [T, N] of y_dtype.  T <= 2^24, N <=
- * 2^24, x_rows >= 1 where T > 0.  first is taken within [0, T]; a row whose input lies outside [0, x_rows) becomes
- * NaN; nothing outside the operands is read or written whatever first and order hold (where
- * first decreases, the rows concerned are unspecified).
+ * 2^24, K <= 2^24, x_rows >= 1 where T > 0.  first is taken within [0, T]; a row whose input
+ * lies outside [0, x_rows) becomes NaN; nothing outside the operands is read or written
+ * whatever first and order hold (where first decreases, the rows concerned are unspecified).
  * Any alignment is taken; rows of a multiple of 16 bytes at multiples of 16 are fastest.
  * Others may first be copied: ws is a device workspace of moe_grouped_matmul_workspace_bytes
  * bytes (0 where nothing is copied; ws may then be NULL), 16-byte aligned, not initialised,
@@ -74,7 +74,7 @@ int moe_mx_grouped_matmul(const moe_mx_rows *x, int32_t x_rows, const moe_mx_row
  * [T, H] of z_dtype; w: [S, k] fp32; place: [S, k] (moe_group's; a position outside [0, T)
  * contributes nothing, whatever its weight); add: [S, H] of z_dtype, or NULL; y: [S, H] of
  * y_dtype.  Rows of z, add and y are ldz, lda and ldy elements apart, at any alignment.  S *
- * k <= 2^24.  S = 0 is a no-op. */
+ * k <= 2^24, H <= 2^30.  S = 0 is a no-op. */
 int moe_combine(const void *z, int32_t z_dtype, int64_t ldz, int32_t T, const float *w, const int32_t *place, int32_t S,
                 int32_t k, int32_t H, const void *add, int64_t lda, void *y, int32_t y_dtype, int64_t ldy,
                 void *stream);

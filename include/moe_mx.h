@@ -37,7 +37,7 @@ extern "C" {
  * at least 0; codes = v / 2^(e-127) rounded to the nearest, ties to the even code, magnitudes
  * over 6 to 6 (MOE_MX_FLOOR cuts off up to a quarter of a block's largest values).  A block
  * of zeros has e = 0; one that holds an infinity or a NaN has e = 255 and codes 0.  A row's
- * last block is filled up with zeros. */
+ * last block is filled up with zeros.  H <= 2^25. */
 enum moe_mx_rounding { MOE_MX_FLOOR = 0, MOE_MX_UP = 1 };
 
 /* q, e of the S rows x [S, H] (x_dtype, any alignment, rows ldx elements apart). */

@@ -198,7 +198,7 @@ int moe_mx_grouped_matmul(const moe_mx_rows *x, int32_t x_rows, const moe_mx_row
 int moe_combine(const void *z, int32_t z_dtype, int64_t ldz, int32_t T, const float *w, const int32_t *place, int32_t S,
                 int32_t k, int32_t H, const void *add, int64_t lda, void *y, int32_t y_dtype, int64_t ldy,
                 void *stream) {
-  if (S < 0 || k < 1 || H < 1 || T < 0 || (int64_t)S * k > kMaxRows) return MOE_EINVAL;
+  if (S < 0 || k < 1 || H < 1 || H > 1 << 30 || T < 0 || (int64_t)S * k > kMaxRows) return MOE_EINVAL;
   if (!known(z_dtype) || !known(y_dtype)) return MOE_EDTYPE;
   if (S == 0) return MOE_OK;
   if ((T > 0 && !z) || !w || !place || !y) return MOE_ENULL;

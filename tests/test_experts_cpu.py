@@ -133,7 +133,8 @@ def combine(z=A, zd=0, ldz=64, T=6, w=A, place=A, S=2, k=3, H=64, add=A, lda=64,
     (dict(S=2 ** 23, k=3), M.MOE_EINVAL), (dict(zd=2), M.MOE_EDTYPE), (dict(yd=2), M.MOE_EDTYPE), (dict(z=None), M.MOE_ENULL),
     (dict(w=None), M.MOE_ENULL), (dict(place=None), M.MOE_ENULL), (dict(y=None), M.MOE_ENULL), (dict(z=A + 2), M.MOE_EINVAL),
     (dict(add=A + 2), M.MOE_EINVAL), (dict(y=A + 2), M.MOE_EINVAL), (dict(w=A + 2), M.MOE_EINVAL), (dict(place=A + 2), M.MOE_EINVAL),
-    (dict(ldz=-1), M.MOE_EINVAL), (dict(lda=-1), M.MOE_EINVAL), (dict(ldy=63), M.MOE_EINVAL), (dict(S=0), M.MOE_OK)])
+    (dict(ldz=-1), M.MOE_EINVAL), (dict(lda=-1), M.MOE_EINVAL), (dict(ldy=63), M.MOE_EINVAL), (dict(S=0), M.MOE_OK),
+    (dict(H=2 ** 30 + 1, ldy=2 ** 30 + 1), M.MOE_EINVAL)])  # columns are counted in 31 bits, whole workgroups of them
 def test_combine_refusals(bad, status):
     assert combine(**bad) == status
 
