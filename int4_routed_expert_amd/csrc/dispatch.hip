@@ -12,7 +12,8 @@ namespace {
 // at a time, finds the lanes that hold the same expert by one ballot a bit, and keeps its own
 // counter per expert in LDS.  Up to kOnePairs pairs one workgroup counts and places all of
 // them; beyond, chunks are counted by one launch and placed by a second, each workgroup of
-// which adds up the counters of the chunks before its own.
+// which adds up the counters of the chunks before its own.  Bound by latency: with 256 experts 8 pairs
+// take 5.4 us, 8192 9.5 (18 in one workgroup), 65536 12.3, 2^21 44 us (0.6 TB/s of the pairs' lists).
 constexpr int kGroupWaves = 16, kGroupThreads = 64 * kGroupWaves;
 constexpr int kOnePairs = 2048;
 constexpr int kMostChunks = 256;
@@ -169,7 +170,9 @@ int64_t chunks_of(int64_t T) { return T <= kOnePairs ? 1 : std::min<int64_t>(kMo
 
 // ---- return --------------------------------------------------------------------------
 // A workgroup takes 2048 columns of a token, eight a lane: it reads its k rows in pieces of 16
-// bytes and adds them up in the order of j.
+// bytes, eight rows on their way at once, and adds them up in the order of j (no atomics: a token's
+// sum does not depend on the others).  Bound by memory: 8192 tokens of 8 rows of 6144 bf16 189 us, 5.3 TB/s;
+// one token 7.9 us in a graph (launch, places, rows: two trips to memory one after the other).
 constexpr int kCombineThreads = 256, kCombineCols = 8 * kCombineThreads;
 
 // Eight columns of a row as they lie (bf16 two to a word), those below H; they are made numbers when they

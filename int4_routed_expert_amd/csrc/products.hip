@@ -202,7 +202,9 @@ __device__ inline void store16(const ProdArgs &a, int64_t i, int n, const uint8_
 // the row of x in runs of 1 KB, 16 bytes a lane: whole cache lines, several runs on their way at once.
 // The matrix instruction wants 16 rows of 64 bytes; it is given 16 pieces of 64 bytes of one row
 // instead, on both sides, and the 16 sums on the diagonal add up to the product (what lies beside it is
-// not used: the matrix cores have time to spare here).
+// not used: the matrix cores have time to spare here).  R = 2 spreads a small matrix over the chip, R = 8
+// reads x less often: microscaled, a token's eight experts of 4096 x 6144 19.4 us (107 MB, 5.5 TB/s) with
+// R = 8, and one row by 4096 x 6144 3.5 us from the caches, 5.0 from memory, with R = 2.
 constexpr int kRun = 1024;
 
 template <Kind KIND, bool ON16>
@@ -271,7 +273,9 @@ __global__ __launch_bounds__(256) void k_product_vec(ProdArgs a, int cols) {
 // ---- straight from memory -----------------------------------------------------------------
 // A workgroup takes 16 weight rows and 16 rows of one expert; its waves share out the row's steps of 64
 // bytes, four of them on their way at once, and add their sums in LDS in a fixed order.  Nothing is
-// staged, so a small product ends after little more than two trips to memory.
+// staged, so a small product ends after little more than two trips to memory: microscaled 77 x 577 x 1120
+// 3.6 us, of which a launch 2.3.  Bound by the weights where rows are few: 32 bf16 rows of 256 experts of
+// 4096 x 6144 239 us (1.5 GB, 6.3 TB/s); by its reads from L2 beyond, where tiles are faster.
 template <Kind KIND, bool ON16>
 __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
   constexpr int kU = 4, kW = 8;
@@ -321,7 +325,13 @@ __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
 // A workgroup takes tiles of BN weight rows x BS rows of one expert, one after another; its WN x WS
 // waves have blocks of 32 x 32 of it, both operands go through LDS in stages of kBK bytes of K, NBUF
 // of them, and a stage's buffer is requested anew as soon as it has been read (as in the int8 product
-// of qmatmul.hip: 16 bytes a lane and 32 cycles an instruction are the same).
+// of qmatmul.hip: 16 bytes a lane and 32 cycles an instruction are the same).  Small tiles for few rows,
+// where starts and padding count; large ones for many, as an operand is read once a tile.
+//
+// Microscaled 8192 x 12288 x 6144: 277 to 294 us (4.2 to 4.5 PFLOP/s; the instructions alone reach 6.4 on such
+// data, by power), 42 us of it starts and ends of tiles, mostly their outputs.  16384 rows of 256 experts, 4096
+// x 6144: 737 us, 4.8 TB/s of weights.  Bf16, 65536 rows of 256 experts, 6144 x 2048: 2.03 to 2.2 ms, 4.2 to 4.5 TB/s
+// with the matrix cores busy for 45 to 52% of it: experts of few rows wait for weights, others for products.
 //
 // The stages of a workgroup's tiles are one stream: while a tile's last stages are multiplied, the
 // first ones of the next tile are on their way, and its outputs leave while they arrive.  (A tile's
@@ -728,9 +738,9 @@ bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && (E == 1 || expert % 16 == 0);
 }
 
-// The kernel with the least estimated time, fitted to 152 measured shapes (us, with the launch; of
-// them it takes the best kernel or one within 8% of it but for eleven, where it loses up to 25%, and
-// 1.4% on average).  Every kernel waits for the weights of the experts that have rows, at 4.4 to 5.6
+// The kernel with the least estimated time, fitted to some 150 measured shapes (us, with the launch; of
+// 151 it takes the best kernel or one within 8% of it but for eleven, where it loses up to 24%, and
+// 1.5% on average).  Every kernel waits for the weights of the experts that have rows, at 4.4 to 5.6
 // TB/s.  The direct kernels: a start, a trip to memory per step of K, and each further workgroup of a
 // compute unit.  Tiles: for each round of them a start and end and a time per stage, `alone` where there
 // is one tile for a compute unit; this and the weights' time add up as squares.  Grouped rows are thought
