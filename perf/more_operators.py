@@ -176,7 +176,7 @@ def _plain_codes(v, up):
     e = torch.where(m > 0, (e + 127).clamp(0, 254), 0)
     a = v.abs().double() / _scales(e)
     c = torch.where(a < 2, (2 * a).round(), torch.where(a < 4, 2 + a.round(), 4 + (a / 2).round())).clamp(max=7).to(torch.uint8)
-    c = c + torch.signbit(v).to(torch.uint8) * 8
+    c = c + 8 * torch.signbit(v)
     return c[..., 0::2] + 16 * c[..., 1::2], e.to(torch.uint8)
 
 
@@ -250,7 +250,8 @@ def _calls(s):
         q, e = (M.mx_silu_quant if case["silu"] else M.mx_quant)(s["x"], round_up=case["up"])
         return M.mx_values(q, e, width=case["H"]), _scales(e)
     if op == "mx":
-        return M.mx_matmul(s["q"], s["e"], s["w"], s["ew"], out_dtype=DTYPES[case["out"]])
+        # the state's codes are wider integers than the bytes that the call takes
+        return M.mx_matmul(s["q"].to(torch.uint8), s["e"], s["w"].to(torch.uint8), s["ew"], out_dtype=DTYPES[case["out"]])
     if op == "dispatch":
         first, order, place = M.group(s["idx"], case["E"])
         return first, order, place, M.combine(s["z"], s["w"], place, add=s["add"], out_dtype=DTYPES[case["out"]])
@@ -258,7 +259,7 @@ def _calls(s):
     plan = {"order": s["order"], "top_k": case["k"]} if case["gather"] else {}
     if op == "grouped":
         return M.grouped_matmul(s["x"], s["w"], s["first"], out_dtype=DTYPES[case["out"]], **plan)
-    return M.mx_grouped_matmul(s["q"], s["e"], s["w"], s["ew"], s["first"], out_dtype=DTYPES[case["out"]], **plan)
+    return M.mx_grouped_matmul(s["q"].to(torch.uint8), s["e"], s["w"], s["ew"], s["first"], out_dtype=DTYPES[case["out"]], **plan)
 
 
 def run(state):
