@@ -734,6 +734,18 @@ struct ProdPlan {
   int64_t ld, bytes_x, bytes;  // of the copies: a row, the rows of x, all
 };
 
+// Row tiles of `rows` rows that T rows of E experts can make.
+int64_t most_tiles(const ProdArgs &a, int rows) {
+  const int64_t whole = ((int64_t)a.T + rows - 1) / rows;
+  return a.first ? a.T / rows + std::min(a.E, a.T) : whole;
+}
+// Column tiles of a launch, 0 where the kernel's row tiles alone are too many.  Tiles are counted in 31 bits,
+// and a direct kernel has a workgroup for each (blocks_of rounds them up): fewer than 2^32 threads.
+int64_t cols_at_once(const ProdArgs &a, const Shape &s) {
+  const int64_t most = s.together ? (int64_t)1 << 30 : (((int64_t)1 << 32) - 1) / s.threads - kXcds;
+  return most / most_tiles(a, s.rows);
+}
+
 bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {
   return (uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0) && (E == 1 || expert % 16 == 0);
 }
@@ -770,6 +782,7 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
   for (int k = 0; k < kTile32; ++k) {
     const Direct &d = kDirect[mx][k];
     const Shape &s = kShapes[k];
+    if (cols_at_once(a, s) == 0) continue;
     const double steps = std::ceil((double)a.row_bytes / d.bytes), cols = std::ceil((double)a.N / s.cols);
     const double tiles = s.rows == 1 ? a.T : a.first ? busy * std::max(1.0, each / s.rows + 0.5) : std::ceil((double)a.T / s.rows);
     const double n = std::ceil(tiles * cols / kUnits) - 1;
@@ -809,11 +822,6 @@ ProdPlan plan_of(const ProdArgs &a, bool mx) {
   return p;
 }
 
-// Row tiles of `rows` rows that T rows of E experts can make.
-int64_t most_tiles(const ProdArgs &a, int rows) {
-  const int64_t whole = ((int64_t)a.T + rows - 1) / rows;
-  return a.first ? a.T / rows + std::min(a.E, a.T) : whole;
-}
 unsigned blocks_of(const ProdArgs &a, int rows, int cols) {
   return (unsigned)((most_tiles(a, rows) * cols + kXcds - 1) / kXcds * kXcds);
 }
@@ -901,11 +909,8 @@ hipError_t launch_product(const ProdArgs &a0, bool mx, hipStream_t st) {
     const hipError_t err = launch_copies(a, p, mx, st);
     if (err != hipSuccess) return err;
   }
-  // Tiles are counted in 31 bits, and a launch of the direct kernels holds fewer than 2^32 threads: many
-  // weight rows go in pieces.
   const Shape &s = kShapes[p.kernel];
-  const int64_t pieces = ((int64_t)1 << 30) / most_tiles(a, s.rows) / (s.together ? 1 : s.threads / 4);
-  const int64_t step = std::max<int64_t>(1, pieces) * s.cols;
+  const int64_t step = cols_at_once(a, s) * s.cols;  // many weight rows go in pieces
   for (int64_t n = 0; n < a.N; n += step) {
     ProdArgs c = a;
     c.N = (int)std::min<int64_t>(step, a.N - n);
