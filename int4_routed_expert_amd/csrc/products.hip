@@ -346,10 +346,13 @@ __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
 // .. 63 blocks 4 .. 7, in both operands.
 // One 16-byte load from base + at straight into LDS, to lds + off + 16 lane (base and lds wave-uniform,
 // off a constant), by the lanes of `lanes`; it is issued, and counted, whichever they are.  All of the
-// wave's lanes are active where it stands.
+// wave's lanes are active where it stands.  A load may read a scalar register that a vector instruction wrote
+// (v_readlane, v_readfirstlane) five instructions later at the earliest, which the compiler does not see to
+// inside assembly; scalar instructions wait for such a write by themselves, so base is copied by one.
 __device__ inline __attribute__((always_inline)) void load_to_lds(uint64_t lanes, const uint8_t *base, uint32_t at, uint32_t lds, int off) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_mov_b64 exec, %4\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
-               ::"s"(lds), "v"(at), "s"(base), "i"(off), "s"(lanes) : "memory", "m0", "scc", "exec");
+  uint64_t from;
+  asm volatile("s_mov_b64 %0, %3\n\ts_add_u32 m0, %1, %4\n\ts_mov_b64 exec, %5\n\tglobal_load_lds_dwordx4 %2, %0\n\ts_mov_b64 exec, -1"
+               : "=&s"(from) : "s"(lds), "v"(at), "s"(base), "i"(off), "s"(lanes) : "memory", "m0", "scc", "exec");
 }
 
 // v, of which the compiler no longer knows what it was: what is derived from it is derived here, and
