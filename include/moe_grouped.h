@@ -51,7 +51,8 @@ typedef struct moe_groups {
  * bf16, rows ldw and experts `expert` elements apart; y: [T, N] of y_dtype.  T <= 2^24, N <=
  * 2^24, K <= 2^24, x_rows >= 1 where T > 0.  first is taken within [0, T]; a row whose input
  * lies outside [0, x_rows) becomes NaN; nothing outside the operands is read or written
- * whatever first and order hold (where first decreases, the rows concerned are unspecified).
+ * whatever first and order hold (where first decreases, the rows that belong to an expert are
+ * unspecified, all of them).
  * Any alignment is taken; rows of a multiple of 16 bytes at multiples of 16 are fastest.
  * Others may first be copied: ws is a device workspace of moe_grouped_matmul_workspace_bytes
  * bytes (0 where nothing is copied; ws may then be NULL), 16-byte aligned, not initialised,

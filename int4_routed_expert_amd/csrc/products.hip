@@ -103,7 +103,8 @@ struct Tiles {
         const int up = __shfl_up(from, o);
         if (lane >= o) from += up;
       }
-      total = __builtin_amdgcn_readlane(from, 63) * cols;
+      // (a `first` that decreases can describe rows many times over)
+      total = (int)min((int64_t)__builtin_amdgcn_readlane(from, 63) * cols, (int64_t)1 << 30);
       from -= n;
     } else {
       total = (a.T + rows - 1) / rows * cols;
@@ -746,7 +747,8 @@ int64_t most_tiles(const ProdArgs &a, int rows) {
 // and a direct kernel has a workgroup for each (blocks_of rounds them up): fewer than 2^32 threads.
 int64_t cols_at_once(const ProdArgs &a, const Shape &s) {
   const int64_t most = s.together ? (int64_t)1 << 30 : (((int64_t)1 << 32) - 1) / s.threads - kXcds;
-  return most / most_tiles(a, s.rows);
+  // row tiles are added up in 31 bits even if every expert has all rows
+  return (int64_t)a.E * ((a.T + s.rows - 1) / s.rows) >> 31 ? 0 : most / most_tiles(a, s.rows);
 }
 
 bool on16(const void *p, int64_t ld, int64_t rows, int64_t expert, int E) {

@@ -27,7 +27,7 @@ def test_weight_rows_in_pieces(S, N, launches):
     assert ran["product_few16"][1] == launches and len(ran) == 1
     a = R.values(q, e)
     step = 1 << 20
-    for n in range(0, N, step):  # one block of whole numbers and quarters: sums are exact in any order
+    for n in range(0, N, step):  # products are multiples of 1/16, their sums below 2^20: exact in any order
         want = a @ R.values(w[n:n + step], ew[n:n + step]).t().contiguous()
         assert torch.equal(y[:, n:n + step], want.to(BF))
         del want
