@@ -57,8 +57,9 @@ class Layer:
             p = self.plain
             gate_up = M.grouped_matmul(x, p["gate_up"], first, order, k)
             z = M.grouped_matmul(M.silu_quant(gate_up, y_dtype=BF, quant=False)[0], p["down"], first)
-            gate_up = x @ p["shared_gate_up"][0].t()
-            shared = M.silu_quant(gate_up, y_dtype=BF, quant=False)[0] @ p["shared_down"][0].t()
+            every = torch.arange(2, dtype=torch.int32, device=x.device) * len(x)  # the shared expert has all rows
+            gate_up = M.grouped_matmul(x, p["shared_gate_up"], every)
+            shared = M.grouped_matmul(M.silu_quant(gate_up, y_dtype=BF, quant=False)[0], p["shared_down"], every)
         return M.combine(z, weights, place, add=shared, out_dtype=torch.float32)
 
 
