@@ -56,7 +56,9 @@ typedef struct moe_groups {
  * Any alignment is taken; rows of a multiple of 16 bytes at multiples of 16 are fastest.
  * Others may first be copied: ws is a device workspace of moe_grouped_matmul_workspace_bytes
  * bytes (0 where nothing is copied; ws may then be NULL), 16-byte aligned, not initialised,
- * used by one call at a time.  T = 0 is a no-op. */
+ * used by one call at a time.  T = 0 is a no-op.
+ * Slow for many rows (ten to twenty times as long): with order, an x of 4 GiB or more from its first
+ * row to its last; rows of x or w 16 MiB or more apart; ldy of 2^22 or more. */
 int64_t moe_grouped_matmul_workspace_bytes(const void *x, int64_t ldx, int32_t x_rows, const void *w, int64_t ldw,
                                            int64_t expert, const moe_groups *g, int32_t T, int32_t N, int32_t K);
 int moe_grouped_matmul(const void *x, int64_t ldx, int32_t x_rows, const void *w, int64_t ldw, int64_t expert,
@@ -64,7 +66,7 @@ int moe_grouped_matmul(const void *x, int64_t ldx, int32_t x_rows, const void *w
                        void *ws, size_t ws_bytes, void *stream);
 
 /* The same of microscaled rows x [x_rows] and weights w [n][N], B blocks each (moe_mx.h: their
- * layout, and what is copied to ws). */
+ * layout, and what is copied to ws; slow for the same distances, of codes or of scales). */
 int64_t moe_mx_grouped_matmul_workspace_bytes(const moe_mx_rows *x, int32_t x_rows, const moe_mx_rows *w,
                                               const moe_groups *g, int32_t T, int32_t N, int32_t B);
 int moe_mx_grouped_matmul(const moe_mx_rows *x, int32_t x_rows, const moe_mx_rows *w, const moe_groups *g, int32_t T,

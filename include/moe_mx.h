@@ -67,7 +67,8 @@ typedef struct moe_mx_rows {
  * that do not lie as their kernels need them (rows of a multiple of 16 bytes at multiples of
  * 16): ws is a device workspace of moe_mx_matmul_workspace_bytes bytes for the same operands
  * (0 where nothing is copied; ws may then be NULL), 16-byte aligned, not initialised, used by
- * one call at a time.  Also MOE_EWORKSPACE. */
+ * one call at a time.  Also MOE_EWORKSPACE.  Slow for many rows (ten to twenty times as long): rows of x
+ * or w 16 MiB or more apart, ldy of 2^22 or more. */
 int64_t moe_mx_matmul_workspace_bytes(const moe_mx_rows *x, const moe_mx_rows *w, int32_t S, int32_t N, int32_t B);
 int moe_mx_matmul(const moe_mx_rows *x, const moe_mx_rows *w, int32_t S, int32_t N, int32_t B, void *y,
                   int32_t y_dtype, int64_t ldy, void *ws, size_t ws_bytes, void *stream);

@@ -53,16 +53,6 @@ __device__ inline f32x16 mfma32(i32x4 a, i32x4 b, int sa, int sb, int step, f32x
   }
 }
 
-// Bytes [k, k + 16) of a row, zeros beyond its end.
-template <Kind KIND>
-__device__ inline i32x4 chunk_at(const uint8_t *row, int k, int row_bytes) {
-  if constexpr (KIND == kMx) {
-    if (k >= row_bytes) return i32x4{0, 0, 0, 0};
-    return load16<true>((const int8_t *)row + k);
-  } else {
-    return load16_tail((const int8_t *)row, k, row_bytes);
-  }
-}
 // The scale of the block at byte k of a row.
 __device__ inline int scale_at(const uint8_t *row, int k, int row_bytes) {
   return k < row_bytes ? ldg<uint8_t>(row + (k >> 4)) : 0;
@@ -208,10 +198,11 @@ __device__ inline void store16(const ProdArgs &a, int64_t i, int n, const uint8_
 // R = 8, and one row by 4096 x 6144 3.5 us from the caches, 5.0 from memory, with R = 2.
 constexpr int kRun = 1024;
 
-template <Kind KIND, bool ON16>
+// Bytes [k, k + 16) of a row, zeros beyond its end.  ON16: the row and its length are multiples of 16 bytes.
+template <bool ON16>
 __device__ inline i32x4 run_at(const uint8_t *row, int k, int row_bytes) {
   if constexpr (ON16) return k < row_bytes ? load16<true>((const int8_t *)row + k) : i32x4{0, 0, 0, 0};
-  else return chunk_at<KIND>(row, k, row_bytes);
+  else return load16_tail((const int8_t *)row, k, row_bytes);
 }
 
 template <Kind KIND, int R, bool ON16>
@@ -241,10 +232,10 @@ __global__ __launch_bounds__(256) void k_product_vec(ProdArgs a, int cols) {
       const int k = k0 + u * kRun + lane * 16;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        W[u][r] = run_at<KIND, ON16>(w[r], k, a.row_bytes);
+        W[u][r] = run_at<ON16>(w[r], k, a.row_bytes);
         if constexpr (KIND == kMx) sw[u][r] = scale_at(we[r], k, a.row_bytes);
       }
-      X[u] = run_at<KIND, ON16>(x, k, a.row_bytes);
+      X[u] = run_at<ON16>(x, k, a.row_bytes);
       if constexpr (KIND == kMx) sx[u] = scale_at(xe, k, a.row_bytes);
     }
 #pragma unroll
@@ -302,8 +293,8 @@ __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int k = s + u < hi ? (s + u) * 64 + kq : a.row_bytes;
-      A[u] = run_at<KIND, ON16>(w, k, a.row_bytes);
-      B[u] = run_at<KIND, ON16>(x, k, a.row_bytes);
+      A[u] = run_at<ON16>(w, k, a.row_bytes);
+      B[u] = run_at<ON16>(x, k, a.row_bytes);
       if constexpr (KIND == kMx) {
         sa[u] = scale_at(we, k, a.row_bytes);
         sb[u] = scale_at(xe, k, a.row_bytes);
@@ -682,7 +673,7 @@ __global__ __launch_bounds__(64 * WN * WS) void k_product_tile(ProdArgs a, int c
     at = next;
     bad = bad_next;
   } while (more);
-  wait_and_meet<0>();  // the last requests, of zeros, have arrived
+  wait_and_meet<0>();  // the last requests, the last tile's first stages once more, have arrived
 }
 
 // ---- rows on 16-byte boundaries -------------------------------------------------------------

@@ -50,8 +50,9 @@ __device__ inline i32x4 load16_tail(const int8_t *row, int k, int K) {
 constexpr int kXcds = 8;
 
 // Where the 16-byte chunk c of a stage's row r lies: the rows' chunks are permuted so that
-// lanes reading one chunk of 16 neighbouring rows spread over all banks (no conflicts are
-// counted; permuted over 8 rows, 8192 x 12288 x 6144 took 611 us where this took 597).
+// lanes reading one chunk of 16 neighbouring rows spread over all banks (the int8 product
+// counts no conflicts; permuted over 8 rows, its 8192 x 12288 x 6144 took 611 us where this
+// took 597).
 constexpr int kBK = 128;
 __device__ inline int mix_of(int r) { return (r >> 1) & 7; }
 __device__ inline int chunk_of(int r, int c) { return r * kBK + ((c ^ mix_of(r)) << 4); }
