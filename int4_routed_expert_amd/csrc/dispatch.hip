@@ -171,8 +171,10 @@ int64_t chunks_of(int64_t T) { return T <= kOnePairs ? 1 : std::min<int64_t>(kMo
 // ---- return --------------------------------------------------------------------------
 // A workgroup takes 2048 columns of a token, eight a lane: it reads its k rows in pieces of 16
 // bytes, eight rows on their way at once, and adds them up in the order of j (no atomics: a token's
-// sum does not depend on the others).  Bound by memory: 8192 tokens of 8 rows of 6144 bf16 189 us, 5.3 TB/s;
-// one token 7.9 us in a graph (launch, places, rows: two trips to memory one after the other).
+// sum does not depend on the others).  Bound by memory: 8192 tokens of 8 rows of 6144 bf16 193 us, 5.2 TB/s,
+// 4096 of 8 fp32 rows of 4096 137 us, 4.9 TB/s; rows off 16 bytes, whose outputs leave one by one: 4096 of 8 rows
+// of 5001 97 us (4.2 TB/s), in fp32 176 (4.7).  One token 7.9 us in a graph (launch, places, rows: two trips to
+// memory one after the other).
 constexpr int kCombineThreads = 256, kCombineCols = 8 * kCombineThreads;
 
 // Eight columns of a row as they lie (bf16 two to a word), those below H; they are made numbers when they

@@ -55,10 +55,11 @@ __device__ inline int scale_of(uint32_t m, int up) {
 
 // A lane has eight neighbours of a block of 32, a quad the block: its largest magnitude takes two
 // exchanges within the quad, and no value leaves its registers.  U units of eight a thread, all of them
-// loaded ahead of the first's arithmetic.  Bound by memory: 8192 x 6144 31.7 us from bf16 (4.0 TB/s), 45.7
-// from fp32 (5.0), where a copy of 1 GiB reaches 5.1; the SwiGLU 68 us (3.3 TB/s) by expf's and the
-// division's instructions, which are those of the other SwiGLUs so that their codes agree.  Rows that
-// start at odd places: 4096 x 5001 16.4 us (3.2 TB/s).  Four rows of 2048: 3.2 us, of which a launch 2.3.
+// loaded ahead of the first's arithmetic.  Bound by memory: 8192 x 6144 30.3 us from bf16 (4.2 TB/s), 45.7
+// from fp32 (5.0), where a copy of 1 GiB reaches 5.1; the SwiGLU 67 us (3.4 TB/s): vector instructions take
+// 72% of the SIMDs' cycles (50% without it), those of expf and the division among them, which are the
+// other SwiGLUs' so that their codes agree.  Rows that start at odd places: 4096 x 5001 16.6 us (3.1 TB/s).
+// Four rows of 2048: 3.2 us, of which a launch 2.3.
 // The conversion divides by its scale operand, a power of two, and rounds once, to the even code at
 // ties, magnitudes over 6 to 6.  With e = 0 that power is no normal number: values and scale are raised by
 // 2^126 first, which is exact.

@@ -194,7 +194,7 @@ __device__ inline void store16(const ProdArgs &a, int64_t i, int n, const uint8_
 // The matrix instruction wants 16 rows of 64 bytes; it is given 16 pieces of 64 bytes of one row
 // instead, on both sides, and the 16 sums on the diagonal add up to the product (what lies beside it is
 // not used: the matrix cores have time to spare here).  R = 2 spreads a small matrix over the chip, R = 8
-// reads x less often: microscaled, a token's eight experts of 4096 x 6144 19.4 us (107 MB, 5.5 TB/s) with
+// reads x less often: microscaled, a token's eight experts of 4096 x 6144 19.9 us (107 MB, 5.4 TB/s) with
 // R = 8, and one row by 4096 x 6144 3.5 us from the caches, 5.0 from memory, with R = 2.
 constexpr int kRun = 1024;
 
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void k_product_vec(ProdArgs a, int cols) {
 // bytes, four of them on their way at once, and add their sums in LDS in a fixed order.  Nothing is
 // staged, so a small product ends after little more than two trips to memory: microscaled 77 x 577 x 1120
 // 3.6 us, of which a launch 2.3.  Bound by the weights where rows are few: 32 bf16 rows of 256 experts of
-// 4096 x 6144 239 us (1.5 GB, 6.3 TB/s); by its reads from L2 beyond, where tiles are faster.
+// 4096 x 6144 240 us (1.41 GB, 5.9 TB/s); by its reads from L2 beyond, where tiles are faster.
 template <Kind KIND, bool ON16>
 __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
   constexpr int kU = 4, kW = 8;
@@ -320,10 +320,11 @@ __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
 // of qmatmul.hip: 16 bytes a lane and 32 cycles an instruction are the same).  Small tiles for few rows,
 // where starts and padding count; large ones for many, as an operand is read once a tile.
 //
-// Microscaled 8192 x 12288 x 6144: 277 to 294 us (4.2 to 4.5 PFLOP/s; the instructions alone reach 6.4 on such
-// data, by power), 42 us of it starts and ends of tiles, mostly their outputs.  16384 rows of 256 experts, 4096
-// x 6144: 737 us, 4.8 TB/s of weights.  Bf16, 65536 rows of 256 experts, 6144 x 2048: 2.03 to 2.2 ms, 4.2 to 4.5 TB/s
-// with the matrix cores busy for 45 to 52% of it: experts of few rows wait for weights, others for products.
+// Microscaled 8192 x 12288 x 6144: 296 us in a graph of such calls (4.2 PFLOP/s; the instructions alone reach 6.4
+// on such data, by power), 281 to 376 in single ones, 317 on average; 42 us of it are starts and ends of tiles,
+// mostly their outputs.  16384 rows of 256 experts, 4096 x 6144: 750 us, 4.6 TB/s of weights.  Bf16, 65536 rows of
+// 256 experts, 6144 x 2048: 1.99 ms in a graph, 2.13 to 2.37 in single calls, 2.20 on average, 4.1 to 4.6 TB/s with
+// the matrix cores busy for 44 to 52% of it: experts of few rows wait for weights, others for products.
 //
 // The stages of a workgroup's tiles are one stream: while a tile's last stages are multiplied, the
 // first ones of the next tile are on their way, and its outputs leave while they arrive.  (A tile's
@@ -335,7 +336,8 @@ __global__ __launch_bounds__(512) void k_product_few(ProdArgs a, int cols) {
 // Microscaled rows add a byte a block: 16 of a row, two stages' worth, are one load into LDS, and a
 // lane reads the four of its blocks of a stage as one word, of which each instruction takes one byte.
 // For that a lane's blocks are neighbours: lanes 0 .. 31 take blocks 0 .. 3 of a stage's eight, lanes 32
-// .. 63 blocks 4 .. 7, in both operands.
+// .. 63 blocks 4 .. 7, in both operands.  Rows r and r + 16 of them meet in a bank: conflicts take 26% (dense)
+// to 29% (grouped) of the cycles in which LDS is read, 4.5% with bf16.
 // One 16-byte load from base + at straight into LDS, to lds + off + 16 lane (base and lds wave-uniform,
 // off a constant), by the lanes of `lanes`; it is issued, and counted, whichever they are.  All of the
 // wave's lanes are active where it stands.  A load may read a scalar register that a vector instruction wrote
